@@ -493,6 +493,165 @@ pkv_status pkv_copy_blocks(void* k_dst, void* v_dst, const pkv_cache_desc* dst, 
                            int32_t num_pairs, pkv_stream_t stream);
 
 /*
+ * Quantised caches: K and V whose scales come from the data.  A cache is
+ * [num_blocks, num_kv_heads, tile], one tile of pkv_quant_tile_bytes bytes
+ * per (block, kv head): the codes of block_size rows (a row = one token's
+ * head_dim elements), for PKV_QUANT_FP4 a scale per 16 elements, and one
+ * binary32 scale per row.  (The source pages name the precision of the cache
+ * as the way to halve its bytes, "KV cache: la memoria de trabajo", section
+ * "Trucos para que el cuaderno sea más fino"; the formats are this library's.)
+ *
+ * A row x of largest magnitude a is stored as (all operations in binary32,
+ * rounded to nearest even):
+ *   PKV_QUANT_INT8   s = a / 127;  code = rint(x / s), value = code * s
+ *   PKV_QUANT_FP4    s = a / 2688; per group of 16 elements of largest
+ *                    magnitude m, t = e4m3(m / (6 s)); code = e2m1(x / (t s))
+ *                    (saturating at +-6), value = code * t * s
+ * A row with a < 2^-80 is stored as zeros; a row that holds an infinity or a
+ * NaN is stored with a NaN scale and reads back as NaN.
+ *
+ * Tile layout: code rows of head_dim (int8: code + 128) or head_dim / 2 bytes
+ * (fp4: the even element in the low half of a byte), 16-byte chunk c of row r
+ * at position c ^ ((r * row_bytes / 128) mod (row_bytes / 16)) of its row;
+ * then (fp4) block_size rows of head_dim / 16 e4m3 scales; then block_size
+ * binary32 row scales.
+ */
+typedef enum { PKV_QUANT_INT8 = 0, PKV_QUANT_FP4 = 1 } pkv_quant_format;
+
+/* Supported: head_dim in {64, 128}; block_size in {8, 16, 32}. */
+typedef struct {
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  pkv_quant_format format;
+} pkv_quant_desc;
+
+/* Bytes of one (block, kv head) tile; 0 for an unsupported geometry. */
+size_t pkv_quant_tile_bytes(int32_t head_dim, int32_t block_size, pkv_quant_format format);
+
+/*
+ * pkv_kv_quantize_and_cache -- pkv_kv_reshape_and_cache into a quantised
+ * cache: each new token's K and V rows are quantised as they are written.
+ *
+ *   k, v        device, [num_tokens, num_kv_heads, head_dim] of src_dtype
+ *               (PKV_F32 or PKV_BF16), 16-byte aligned
+ *   k_cache, v_cache  device, [num_blocks, num_kv_heads, tile], 16-byte aligned
+ *   slot_mapping device int64 [num_tokens]; negative = skip the token;
+ *               >= num_blocks * block_size sets PKV_DEVERR_BAD_SLOT and skips
+ * Two tokens with the same slot in one call race.
+ */
+pkv_status pkv_kv_quantize_and_cache(const void* k, const void* v, pkv_dtype src_dtype, int32_t num_tokens,
+                                     void* k_cache, void* v_cache, const pkv_quant_desc* cache,
+                                     const int64_t* slot_mapping, pkv_stream_t stream);
+
+/*
+ * pkv_gather_kv_quant -- read a quantised cache back: pkv_gather_kv with the
+ * values that the codes stand for, code * scale in binary32, rounded once
+ * more (to nearest even) for PKV_BF16.
+ *
+ *   k_out, v_out  device [total_tokens, num_kv_heads, head_dim] of out_dtype
+ *                 (PKV_F32 or PKV_BF16), 16-byte aligned
+ *   cu_seq_lens   device int64 [num_seqs + 1], the first row of each sequence
+ *   total_tokens  rows of k_out and v_out: a token past them is not written
+ *                 (PKV_DEVERR_BAD_SEQ_LEN)
+ *   max_seq_len   host upper bound of seq_lens (a longer sequence sets
+ *                 PKV_DEVERR_BAD_SEQ_LEN and is clipped, as is one longer
+ *                 than its table); rows of a block outside the pool are left
+ *                 as they were (PKV_DEVERR_BAD_BLOCK_ID)
+ */
+pkv_status pkv_gather_kv_quant(void* k_out, void* v_out, pkv_dtype out_dtype, const void* k_cache,
+                               const void* v_cache, const pkv_quant_desc* cache, const int32_t* block_tables,
+                               int32_t max_blocks_per_seq, const int32_t* seq_lens, const int64_t* cu_seq_lens,
+                               int32_t num_seqs, int64_t total_tokens, int32_t max_seq_len, pkv_stream_t stream);
+
+/*
+ * pkv_score_opts -- how pkv_paged_attention_scored and
+ * pkv_paged_attention_quant change the scores.  For a query row at position p
+ * of its sequence (of length L) and query head qh, over positions t:
+ *   x_t = scale * q . K[t]
+ *   y_t = softcap * tanh(x_t / softcap)          (softcap > 0; else x_t)
+ *   z_t = y_t - alibi_slopes[qh] * |p - t|       (alibi_slopes given; else y_t)
+ *   t is attended iff t < L and
+ *       (t <= p and (window_tokens == 0 or t > p - window_tokens or t < sink_tokens))
+ *       or t < prefix_lens[s]
+ *   out = sum_t softmax(z)_t V[t] over the attended t (a zero row if there is none)
+ * A prefix is attended by every row of its sequence in both directions (a
+ * prefix-LM's prompt) and through any window.  Zero-initialise the struct for
+ * plain scores.
+ *   softcap       >= 0, finite; 0 = no cap
+ *   alibi_slopes  device fp32 [num_q_heads], or NULL
+ *   prefix_lens   device int32 [num_seqs], or NULL; a negative length is 0,
+ *                 one beyond L is L
+ *   window_tokens >= 0 (0 = no window); sink_tokens >= 0, ignored without a window
+ */
+typedef struct {
+  float softcap;
+  const float* alibi_slopes;
+  const int32_t* prefix_lens;
+  int32_t window_tokens;
+  int32_t sink_tokens;
+} pkv_score_opts;
+
+/*
+ * pkv_scored_workspace_bytes -- device workspace of pkv_paged_attention_scored
+ * and pkv_paged_attention_quant on the current device (0 for invalid sizes or
+ * no device): 1 MiB that these calls leave alone (the merge counters of the
+ * other calls' workspaces), then two partial results per thread block of the
+ * largest grid.  The contents need not be set.
+ *   max_q   the largest number of query tokens of one sequence (1 for decode)
+ */
+size_t pkv_scored_workspace_bytes(int32_t num_seqs, int32_t max_q, int32_t num_q_heads, int32_t num_kv_heads,
+                                  int32_t head_dim);
+
+/*
+ * pkv_paged_attention_scored -- paged attention with modified scores
+ * (pkv_score_opts) over a bf16 or fp8-e4m3 cache, for one query token per
+ * sequence (q_start NULL: decode) or several (prompt chunks, verification).
+ *
+ *   out, q        device bf16 (q_dtype PKV_BF16), 16-byte aligned:
+ *                 [num_seqs, num_q_heads, head_dim] without q_start, the row
+ *                 of sequence s at position seq_lens[s] - 1; with q_start
+ *                 [total_q, num_q_heads, head_dim], sequence s owning rows
+ *                 q_start[s] .. q_start[s + 1] - 1, its last positions.
+ *                 Rows of no sequence are left as they were
+ *   q_start       device int32 [num_seqs + 1] as in pkv_paged_attention_multi,
+ *                 or NULL
+ *   total_q       rows of q and out (num_seqs when q_start is NULL)
+ *   max_q         host upper bound of a sequence's query rows (ignored when
+ *                 q_start is NULL); a sequence with more, with more than
+ *                 seq_lens[s], or with rows past total_q sets
+ *                 PKV_DEVERR_BAD_SEQ_LEN, its rows left as they were
+ *   caches, tables, seq_lens, max_seq_len, scale, kv_scale
+ *                 as in pkv_paged_attention_decode; PKV_F32 caches give
+ *                 PKV_ERR_UNSUPPORTED (the products run on the tensor cores).
+ *                 Blocks that no row attends are not read, nor their entries
+ *   opts          NULL = plain scores
+ *   workspace     >= pkv_scored_workspace_bytes(...) bytes, 256-byte aligned.
+ *                 Calls sharing one workspace must not overlap on the GPU
+ */
+pkv_status pkv_paged_attention_scored(void* out, const void* q, pkv_dtype q_dtype, const int32_t* q_start,
+                                      int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_q_heads,
+                                      const void* k_cache, const void* v_cache, const pkv_cache_desc* cache,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* seq_lens, int32_t max_seq_len, float scale, float kv_scale,
+                                      const pkv_score_opts* opts, void* workspace, size_t workspace_bytes,
+                                      pkv_stream_t stream);
+
+/*
+ * pkv_paged_attention_quant -- pkv_paged_attention_scored over a quantised
+ * cache (pkv_kv_quantize_and_cache).  The codes enter the products exactly;
+ * the row scales multiply the scores and the probabilities.
+ */
+pkv_status pkv_paged_attention_quant(void* out, const void* q, pkv_dtype q_dtype, const int32_t* q_start,
+                                     int32_t num_seqs, int32_t total_q, int32_t max_q, int32_t num_q_heads,
+                                     const void* k_cache, const void* v_cache, const pkv_quant_desc* cache,
+                                     const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                     const int32_t* seq_lens, int32_t max_seq_len, float scale,
+                                     const pkv_score_opts* opts, void* workspace, size_t workspace_bytes,
+                                     pkv_stream_t stream);
+
+/*
  * pkv_get_device_error -- synchronise `stream`, then read and clear the
  * current device's error word (PKV_DEVERR_* bits) into *code_out.
  */

@@ -17,6 +17,14 @@ Entry points (same names as the C ABI, without the ``pkv_`` prefix):
 * :func:`gather_kv` -- contiguous copy of every sequence's cached tokens;
 * :func:`copy_blocks` -- whole-block copies between pools (copy-on-write of a
   shared block, swap to pinned host memory and back);
+* :func:`kv_quantize_and_cache` / :func:`gather_kv_quant` -- a quantised (int8
+  or fp4) cache whose scales come from the data: tokens quantised as they are
+  written, and read back (:func:`quant_cache_shape`, :func:`quant_tile_bytes`);
+* :func:`paged_attention_quant` -- attention over a quantised cache, one query
+  token per sequence or several;
+* :func:`paged_attention_scored` -- attention over a bf16 or fp8 cache with
+  modified scores: a tanh cap, a distance bias, a window, a prefix that every
+  row sees (:func:`paged_attention_quant` takes the same options);
 * :func:`decode_workspace_bytes`, :func:`get_device_error`;
 * :func:`set_decode_engine` / :func:`get_decode_engine` (and the
   :func:`decode_engine` context manager) -- tensor cores (default) or CUDA
@@ -44,6 +52,8 @@ __all__ = [
     "DEVERR_BAD_SEQ_LEN", "DEVERR_WAIT_TIMEOUT", "DEVERR_SMEM_ALIGN", "set_decode_engine",
     "get_decode_engine", "decode_engine", "ENGINE_TENSOR_CORES", "ENGINE_CUDA_CORES",
     "set_tcgen05", "get_tcgen05", "tcgen05", "selftest_wait_timeout",
+    "QuantDesc", "ScoreOpts", "QUANT_FORMATS", "quant_tile_bytes", "quant_cache_shape", "kv_quantize_and_cache",
+    "gather_kv_quant", "paged_attention_scored", "paged_attention_quant", "scored_workspace_bytes",
 ]
 
 F32, BF16, FP8_E4M3 = 0, 1, 2
@@ -73,6 +83,20 @@ class CacheDesc(ctypes.Structure):
                 ("dtype", ctypes.c_int)]
 
 
+class QuantDesc(ctypes.Structure):
+    _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("format", ctypes.c_int)]
+
+
+class ScoreOpts(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("alibi_slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p),
+                ("window_tokens", ctypes.c_int32), ("sink_tokens", ctypes.c_int32)]
+
+
+QUANT_FORMATS = {"int8": 0, "fp4": 1}
+
+
 def library() -> ctypes.CDLL:
     """Load libpkv.so (raises if it has not been built)."""
     global _lib
@@ -84,7 +108,7 @@ def library() -> ctypes.CDLL:
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
         lib = ctypes.CDLL(library_path)
         vp, i32, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
-        desc = ctypes.POINTER(CacheDesc)
+        desc, qdesc, opts = (ctypes.POINTER(c) for c in (CacheDesc, QuantDesc, ScoreOpts))
         sigs = {
             "pkv_kv_reshape_and_cache": [vp, vp, ctypes.c_int, i32, vp, vp, desc, vp, f32, vp],
             "pkv_decode_workspace_bytes": [i32, i32, i32, i32, i32, i32],
@@ -102,6 +126,14 @@ def library() -> ctypes.CDLL:
             "pkv_multi_workspace_bytes": [i32, i32, i32, i32, i32, i32],
             "pkv_paged_attention_multi": [vp, vp, ctypes.c_int, vp, i32, i32, i32, i32, vp, vp, desc, vp, i32,
                                           vp, i32, f32, f32, vp, sz, vp],
+            "pkv_quant_tile_bytes": [i32, i32, ctypes.c_int],
+            "pkv_kv_quantize_and_cache": [vp, vp, ctypes.c_int, i32, vp, vp, qdesc, vp, vp],
+            "pkv_gather_kv_quant": [vp, vp, ctypes.c_int, vp, vp, qdesc, vp, i32, vp, vp, i32, ctypes.c_int64, i32, vp],
+            "pkv_scored_workspace_bytes": [i32, i32, i32, i32, i32],
+            "pkv_paged_attention_scored": [vp, vp, ctypes.c_int, vp, i32, i32, i32, i32, vp, vp, desc, vp, i32,
+                                           vp, i32, f32, f32, opts, vp, sz, vp],
+            "pkv_paged_attention_quant": [vp, vp, ctypes.c_int, vp, i32, i32, i32, i32, vp, vp, qdesc, vp, i32,
+                                          vp, i32, f32, opts, vp, sz, vp],
             "pkv_get_device_error": [ctypes.POINTER(ctypes.c_uint32), vp],
             "pkv_copy_blocks": [vp, vp, desc, vp, vp, desc, vp, i32, vp],
             "pkv_status_string": [ctypes.c_int],
@@ -119,6 +151,8 @@ def library() -> ctypes.CDLL:
         lib.pkv_decode_workspace_bytes.restype = sz
         lib.pkv_cascade_workspace_bytes.restype = sz
         lib.pkv_multi_workspace_bytes.restype = sz
+        lib.pkv_quant_tile_bytes.restype = sz
+        lib.pkv_scored_workspace_bytes.restype = sz
         lib.pkv_status_string.restype = ctypes.c_char_p
         lib.pkv_set_tcgen05.argtypes = [i32]
         lib.pkv_set_tcgen05.restype = None
@@ -487,6 +521,202 @@ def copy_blocks(k_dst: torch.Tensor, v_dst: torch.Tensor, k_src: torch.Tensor, v
     _check(library().pkv_copy_blocks(_addr(k_dst), _addr(v_dst), ctypes.byref(dd), _addr(k_src), _addr(v_src),
                                      ctypes.byref(sd), _addr(block_pairs), int(block_pairs.shape[0]),
                                      _stream(stream)), "copy_blocks")
+
+
+# ------------------------------------------------------------------ quantised caches, modified scores
+@contextlib.contextmanager
+def _launching(stream, *tensors):
+    """The device of the call's tensors made current (they must share one),
+    and the stream the call runs on; allocations inside belong to it."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or not next(iter(devices)).type == "cuda":
+        raise ValueError("tensors must live on one CUDA device")
+    device = next(iter(devices))
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        else:
+            with torch.cuda.stream(stream):
+                yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _int(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, numel: Optional[int] = None) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype)[6:]}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries, got {t.numel()}")
+
+
+def _format(fmt: str) -> int:
+    try:
+        return QUANT_FORMATS[fmt]
+    except KeyError:
+        raise ValueError(f"unknown quantised format {fmt!r}: one of {', '.join(QUANT_FORMATS)}") from None
+
+
+def quant_tile_bytes(head_dim: int, block_size: int, fmt: str) -> int:
+    """Bytes of one (block, kv head) tile of a quantised cache."""
+    n = int(library().pkv_quant_tile_bytes(head_dim, block_size, _format(fmt)))
+    if n == 0:
+        raise ValueError(f"unsupported geometry: head_dim {head_dim}, block_size {block_size}")
+    return n
+
+
+def quant_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int, fmt: str):
+    """Shape of the uint8 tensor that holds a quantised K (or V) cache."""
+    return (num_blocks, num_kv_heads, quant_tile_bytes(head_dim, block_size, fmt))
+
+
+def _quant_desc(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size: int, head_dim: int, fmt: str) -> QuantDesc:
+    tile = quant_tile_bytes(head_dim, block_size, fmt)
+    for c in (k_cache, v_cache):
+        if c.dtype != torch.uint8 or c.dim() != 3 or c.shape[2] != tile:
+            raise ValueError(f"quantised caches are uint8 [num_blocks, num_kv_heads, {tile}]")
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    return QuantDesc(k_cache.shape[0], block_size, k_cache.shape[1], head_dim, _format(fmt))
+
+
+def kv_quantize_and_cache(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          slot_mapping: torch.Tensor, block_size: int, fmt: str = "int8", stream=None) -> None:
+    """Quantise ``k, v [T, Hkv, d]`` into the slots ``slot_mapping`` (int64;
+    negative = skip) of a quantised cache (:func:`quant_cache_shape`).
+
+    ``"int8"``: one scale per (token, kv head); ``"fp4"``: e2m1 codes with an
+    e4m3 scale per 16 elements and one scale per (token, kv head).  The scales
+    come from the rows themselves.  A row with an infinity or a NaN reads back
+    as NaN."""
+    if k.dtype not in (torch.float32, torch.bfloat16) or v.dtype != k.dtype:
+        raise TypeError("k and v must both be float32 or bfloat16")
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v are [num_tokens, num_kv_heads, head_dim]")
+    _int("slot_mapping", slot_mapping, torch.int64, k.shape[0])
+    desc = _quant_desc(k_cache, v_cache, block_size, int(k.shape[2]), fmt)
+    if desc.num_kv_heads != k.shape[1]:
+        raise ValueError(f"the cache has {desc.num_kv_heads} kv heads, k has {k.shape[1]}")
+    with _launching(stream, k, v, k_cache, v_cache, slot_mapping) as st:
+        _check(library().pkv_kv_quantize_and_cache(
+            _ptr(k), _ptr(v), _dt(k), int(k.shape[0]), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc),
+            _ptr(slot_mapping), st), "kv_quantize_and_cache")
+
+
+def gather_kv_quant(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                    block_size: int, head_dim: int, fmt: str, max_seq_len: int,
+                    out_dtype: torch.dtype = torch.bfloat16, cu_seq_lens: Optional[torch.Tensor] = None,
+                    total_tokens: Optional[int] = None, stream=None):
+    """The values of every sequence's cached tokens, ``[sum(seq_lens), Hkv, d]``
+    in ``out_dtype`` (float32 or bfloat16).  Without ``cu_seq_lens`` and
+    ``total_tokens`` they are read from ``seq_lens`` (with a synchronisation)."""
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    B = seq_lens.numel()
+    _int("block_tables", block_tables, torch.int32)
+    _int("seq_lens", seq_lens, torch.int32)
+    _int("cu_seq_lens", cu_seq_lens, torch.int64, B + 1)
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    desc = _quant_desc(k_cache, v_cache, block_size, head_dim, fmt)
+    with _launching(stream, k_cache, v_cache, block_tables, seq_lens, cu_seq_lens) as st:
+        if cu_seq_lens is None:
+            cu_seq_lens = torch.zeros(B + 1, dtype=torch.int64, device=seq_lens.device)
+            cu_seq_lens[1:] = torch.cumsum(seq_lens.to(torch.int64), 0)
+        if total_tokens is None:
+            total_tokens = int(cu_seq_lens[-1].item())
+        k_out = torch.empty((total_tokens, desc.num_kv_heads, head_dim), dtype=out_dtype, device=k_cache.device)
+        v_out = torch.empty_like(k_out)
+        _check(library().pkv_gather_kv_quant(
+            _ptr(k_out), _ptr(v_out), _dt(k_out), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc),
+            _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens), _ptr(cu_seq_lens), B, total_tokens,
+            int(max_seq_len), st), "gather_kv_quant")
+    return k_out, v_out
+
+
+def scored_workspace_bytes(num_seqs: int, max_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Workspace of :func:`paged_attention_scored` and :func:`paged_attention_quant`
+    (``max_q`` 1 for one query token per sequence)."""
+    return int(library().pkv_scored_workspace_bytes(num_seqs, max_q, num_q_heads, num_kv_heads, head_dim))
+
+
+def _attend(call, what, desc, kv_scale, out, q, k_cache, v_cache, block_tables, seq_lens, scale, q_start, max_q, softcap,
+            alibi_slopes, window, sinks, prefix_lens, max_seq_len, workspace, stream):
+    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out are [rows, num_q_heads, head_dim] of one type")
+    total, Hq, d = q.shape
+    if d != desc.head_dim:
+        raise ValueError(f"q has head_dim {d}, the cache {desc.head_dim}")
+    B = seq_lens.numel()
+    _int("block_tables", block_tables, torch.int32)
+    _int("seq_lens", seq_lens, torch.int32)
+    _int("q_start", q_start, torch.int32, B + 1)
+    _int("prefix_lens", prefix_lens, torch.int32, B)
+    _int("alibi_slopes", alibi_slopes, torch.float32, Hq)
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    if q_start is None and total != B:
+        raise ValueError("q must have one row per sequence (or q_start given)")
+    mbps = int(block_tables.shape[1])
+    if max_seq_len is None:
+        max_seq_len = mbps * desc.block_size
+    with _launching(stream, out, q, k_cache, v_cache, block_tables, seq_lens, q_start, alibi_slopes, prefix_lens) as st:
+        if q_start is None:
+            max_q = 1
+        elif max_q is None:
+            max_q = int((q_start[1:] - q_start[:-1]).max().item()) if B else 0
+        opts = ScoreOpts(float(softcap), _ptr(alibi_slopes), _ptr(prefix_lens), int(window), int(sinks))
+        nbytes = scored_workspace_bytes(B, max_q, Hq, desc.num_kv_heads, d)
+        # without a workspace of the caller's the call has one of its own: calls
+        # on several streams and captured graphs then share nothing
+        ws = (torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device) if workspace is None
+              else workspace.get(nbytes))
+        qdt = F32 if q.dtype == torch.float32 else _dt(q)
+        args = [_ptr(out), _ptr(q), qdt, _ptr(q_start), B, total, int(max_q), Hq, _ptr(k_cache), _ptr(v_cache),
+                ctypes.byref(desc), _ptr(block_tables), mbps, _ptr(seq_lens), int(max_seq_len), float(scale)]
+        if kv_scale is not None:
+            args.append(float(kv_scale))
+        _check(call(*args, ctypes.byref(opts), _ptr(ws), ws.numel(), st), what)
+    return out
+
+
+def paged_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float, kv_scale: float = 1.0,
+                           q_start: Optional[torch.Tensor] = None, max_q: Optional[int] = None, softcap: float = 0.0,
+                           alibi_slopes: Optional[torch.Tensor] = None, window: int = 0, sinks: int = 0,
+                           prefix_lens: Optional[torch.Tensor] = None, max_seq_len: Optional[int] = None,
+                           workspace: Optional[DecodeWorkspace] = None, stream=None) -> torch.Tensor:
+    """Paged attention with modified scores over a bf16 or fp8 cache: one query
+    row per sequence (decode), or with ``q_start`` (int32 ``[B + 1]``) several,
+    as in :func:`paged_attention_multi`.
+
+    For a row at position p and query head h, position t scores
+    ``cap(scale * q . K[t]) - alibi_slopes[h] * |p - t|`` with ``cap(x) =
+    softcap * tanh(x / softcap)`` (``softcap`` 0: no cap), and is attended iff
+    ``t <= p`` and (no ``window``, or ``t > p - window``, or ``t < sinks``), or
+    ``t < prefix_lens[s]``.  ``max_q`` is a host bound of the rows per sequence
+    (read from ``q_start`` with a synchronisation when omitted)."""
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have the same shape and dtype")
+    return _attend(library().pkv_paged_attention_scored, "paged_attention_scored", _desc(k_cache, None), kv_scale, out,
+                   q, k_cache, v_cache, block_tables, seq_lens, scale, q_start, max_q, softcap, alibi_slopes, window,
+                   sinks, prefix_lens, max_seq_len, workspace, stream)
+
+
+def paged_attention_quant(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float, block_size: int,
+                          fmt: str = "int8", q_start: Optional[torch.Tensor] = None, max_q: Optional[int] = None,
+                          softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None, window: int = 0,
+                          sinks: int = 0, prefix_lens: Optional[torch.Tensor] = None,
+                          max_seq_len: Optional[int] = None, workspace: Optional[DecodeWorkspace] = None,
+                          stream=None) -> torch.Tensor:
+    """:func:`paged_attention_scored` over a quantised cache
+    (:func:`kv_quantize_and_cache`; ``block_size`` and ``fmt`` as there)."""
+    desc = _quant_desc(k_cache, v_cache, block_size, int(q.shape[-1]), fmt)
+    return _attend(library().pkv_paged_attention_quant, "paged_attention_quant", desc, None, out, q, k_cache, v_cache,
+                   block_tables, seq_lens, scale, q_start, max_q, softcap, alibi_slopes, window, sinks, prefix_lens,
+                   max_seq_len, workspace, stream)
 
 
 def selftest_wait_timeout(stream=None) -> None:

@@ -1,0 +1,8 @@
+// Column-attention instances (attn_cols.cuh): fp8 caches, head_dim 128.
+#include "attn_cols.cuh"
+
+namespace pkv {
+namespace cols {
+Kernel pick_fp8_128(int bs, int nt) { return pick<kFp8, 128>(bs, nt); }
+}  // namespace cols
+}  // namespace pkv

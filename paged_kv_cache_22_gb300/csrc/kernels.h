@@ -60,6 +60,9 @@ struct CopyBlocksArgs {
   int64_t num_pairs;
 };
 
+// The device error word of a device (pkv_api.cu); null if it has none.
+unsigned int* device_error_word(int dev);
+
 cudaError_t launch_copy_blocks(const CopyBlocksArgs& a, cudaStream_t stream);
 cudaError_t launch_reshape_and_cache(const ReshapeArgs& a, int src_is_bf16, cudaStream_t stream);
 cudaError_t launch_gather_kv(const GatherArgs& a, int max_seq_len, cudaStream_t stream);
