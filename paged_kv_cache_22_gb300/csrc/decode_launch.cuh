@@ -81,6 +81,10 @@ bool find_decode_mq(pkv_dtype dt, int head_dim, int block_size, DecodeKernel* ou
 bool encode_cache_maps(const DecodeKernel& k, const pkv_cache_desc* cache, const void* k_cache,
                        const void* v_cache, TmaMaps* maps);
 
+// The tensor maps of kernels whose copies land as tcgen05 operands (pkv_api.cu):
+// bf16, one 128-byte span of a block per box; fp8, a block's whole rows.
+bool encode_operand_maps(const pkv_cache_desc* cache, const void* k_cache, const void* v_cache, TmaMaps* maps);
+
 // Fill `out` with the instance for (D, BS, G, balanced); false if not built.
 // One finder per cache type, engine and REMAP, each in its own translation
 // unit (they compile in parallel).

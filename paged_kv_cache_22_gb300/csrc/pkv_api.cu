@@ -250,6 +250,10 @@ bool encode_cache_maps(const DecodeKernel& k, const pkv_cache_desc* cache, const
   return encode_cache_map(cache, k_cache, &maps->k) && encode_cache_map(cache, v_cache, &maps->v);
 }
 
+bool encode_operand_maps(const pkv_cache_desc* cache, const void* k_cache, const void* v_cache, TmaMaps* maps) {
+  return encode_tc05_maps(cache, k_cache, v_cache, maps);
+}
+
 }  // namespace pkv
 
 using namespace pkv;

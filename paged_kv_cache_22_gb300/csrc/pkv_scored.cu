@@ -8,6 +8,7 @@
 #include <utility>
 
 #include "attn_cols.cuh"
+#include "attn_tiles.cuh"
 #include "decode_launch.cuh"
 #include "kernels.h"
 
@@ -22,20 +23,23 @@ bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p
 // the 8-column instance, more the 16-column one.
 int column_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
+// Query rows of a (sequence, kv head) from which a call takes the 128-row tiles.
+constexpr int64_t kTileRows = 128;
+
 // CTAs per SM the workspace is sized for.
 int max_ctas_per_sm(int nt) { return nt == 1 ? 16 : 8; }
 
 // Opt a kernel into its dynamic shared memory once per device; its CTAs per SM.
-int prepare(const cols::Kernel& k, int dev) {
+int prepare(const void* fn, int threads, int smem, int dev) {
   static std::mutex mu;
   static std::map<std::pair<const void*, int>, int> known;
   std::lock_guard<std::mutex> lk(mu);
-  const auto key = std::make_pair(k.fn, dev);
+  const auto key = std::make_pair(fn, dev);
   const auto it = known.find(key);
   if (it != known.end()) return it->second;
   int occ = 0;
-  if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.fn, 32, k.smem) != cudaSuccess)
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, smem) != cudaSuccess)
     return 0;
   known[key] = occ;
   return occ;
@@ -47,6 +51,15 @@ cols::Kernel pick_kernel(int kind, int D, int bs, int nt) {
     case cols::kFp8: return D == 64 ? cols::pick_fp8_64(bs, nt) : cols::pick_fp8_128(bs, nt);
     case cols::kInt8: return D == 64 ? cols::pick_int8_64(bs, nt) : cols::pick_int8_128(bs, nt);
     default: return D == 64 ? cols::pick_fp4_64(bs, nt) : cols::pick_fp4_128(bs, nt);
+  }
+}
+
+tiles::Kernel pick_tile_kernel(int kind, int D, int bs) {
+  switch (kind) {
+    case cols::kBf16: return tiles::pick_bf16(D, bs);
+    case cols::kFp8: return tiles::pick_fp8(D, bs);
+    case cols::kInt8: return tiles::pick_int8(D, bs);
+    default: return tiles::pick_fp4(D, bs);
   }
 }
 
@@ -78,12 +91,11 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   const int nt = column_tiles(rows), nc = 8 * nt;
   const int64_t chunks = (rows + nc - 1) / nc;
   if (rows > (1 << 30) || num_seqs * chunks > (1 << 30)) return PKV_ERR_UNSUPPORTED;
-  const cols::Kernel k = pick_kernel(kind, D, bs, nt);
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
   unsigned int* err = device_error_word(dev);
-  const int sms = pkv_device_sm_count(), occ = prepare(k, dev);
-  if (!err || sms <= 0 || occ <= 0) return PKV_ERR_CUDA;
+  const int sms = pkv_device_sm_count();
+  if (!err || sms <= 0) return PKV_ERR_CUDA;
   const size_t need = pkv_scored_workspace_bytes(num_seqs, q_start ? max_q : 1, num_q_heads, desc.num_kv_heads, D);
   if (!workspace || workspace_bytes < need) return PKV_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return PKV_ERR_INVALID_ARG;
@@ -120,6 +132,19 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounters);
 
   TmaMaps maps{};
+  if (q_start && rows >= kTileRows && num_seqs <= 65535 && desc.num_kv_heads <= 65535) {
+    const tiles::Kernel t = pick_tile_kernel(kind, D, bs);
+    if (prepare(t.fn, tiles::kThreads, t.smem, dev) <= 0) return PKV_ERR_CUDA;
+    if ((kind == cols::kBf16 || kind == cols::kFp8) && !encode_operand_maps(&desc, k_cache, v_cache, &maps))
+      return PKV_ERR_CUDA;
+    const dim3 grid((unsigned)((rows + 2 * tiles::kTile - 1) / (2 * tiles::kTile)), (unsigned)desc.num_kv_heads,
+                    (unsigned)num_seqs);
+    void* args[] = {&a, &maps};
+    return cudaLaunchKernel(t.fn, grid, dim3(tiles::kThreads), args, t.smem, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  }
+  const cols::Kernel k = pick_kernel(kind, D, bs, nt);
+  const int occ = prepare(k.fn, 32, k.smem, dev);
+  if (occ <= 0) return PKV_ERR_CUDA;
   if (kind == cols::kBf16 || kind == cols::kFp8) {
     DecodeKernel dk;
     dk.tensor_maps = true;

@@ -7,7 +7,9 @@ the weights moves a convex combination by.  fp8 and quantised caches hold a
 weight in fp16 (2^-11 of it), bf16 caches in two bf16 parts (2^-17); the scores
 come from exact products summed in fp32, their errors (and those of exp2,
 tanh) are below 2^-12 of a weight at these sizes.  So 2^-8 |o| + 2^-10 V and
-2^-8 |o| + 2^-11 V."""
+2^-8 |o| + 2^-11 V.  Calls with 128 or more query rows per (sequence, kv head)
+hold a weight over a bf16 cache in one bf16 part (2^-8 of it): 2^-8 |o| +
+(2^-8 + 2^-11) V."""
 from __future__ import annotations
 
 import math
@@ -82,6 +84,7 @@ class Problem:
         tables = (self.tables if tables is None else tables).to(DEV)
         ln = torch.tensor(self.lens if lens is None else lens, dtype=torch.int32, device=DEV)
         qs = self.q_start if q_start is None else q_start
+        self.bound = max_q or max(self.rows or [1])
         opts = {k: v.to(DEV) if isinstance(v, torch.Tensor) else v for k, v in opts.items()}
         kw = dict(q_start=None if qs is None else qs.to(DEV), max_q=max_q, workspace=workspace, stream=stream,
                   max_seq_len=max_seq_len or max(max(self.lens), 1), **opts)
@@ -113,11 +116,17 @@ class Problem:
             base += L
         return want, vmax
 
+    def weights(self):
+        if self.kind != "bf16":
+            return 2.0 ** -10
+        tiled = self.rows is not None and self.bound * (self.hq // self.hkv) >= 128
+        return 2.0 ** -11 + (2.0 ** -8 if tiled else 0.0)
+
     def check(self, got, want, vmax, what=""):
         torch.cuda.synchronize()
         got = got.double().cpu().numpy()
         assert np.array_equal(np.isnan(got), np.isnan(want)), what + ": NaN in other places"
-        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 if self.kind == "bf16" else 2.0 ** -10) * vmax
+        tol = 2.0 ** -8 * np.abs(want) + self.weights() * vmax
         over = np.nan_to_num(np.abs(got - want) - tol)
         i = np.unravel_index(over.argmax(), over.shape)
         assert over.max() <= 0, f"{what}: at {i}: {got[i]} for {want[i]}, tolerance {tol[i]}"
@@ -194,6 +203,52 @@ def test_long_chunk(pkv, kind):
     for o in ({}, dict(softcap=10.0, window=50, prefix_lens=torch.tensor([60, 0], dtype=torch.int32))):
         p.check(p.run(**o), *p.expected(**o), kind)
     assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("opt", list(OPTS))
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "d%d_bs%d_q%d_kv%d" % s)
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_of_query_rows(pkv, kind, shape, opt):
+    """Calls whose bound asks for 128-row tiles: ragged chunks of zero rows to
+    several tiles, over one to several steps of 128 positions."""
+    d, bs, hq, hkv = shape
+    lens, rows = [300, 129, 128, 1, 77, 515], [90, 1, 128, 1, 0, 3]
+    p = Problem(pkv, kind, d, bs, hq, hkv, lens, rows, seed=d + bs + 2)
+    o = options(OPTS[opt], hq, lens)
+    p.check(p.run(**o), *p.expected(**o), f"{kind} {shape} {opt}")
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_whose_maximum_grows(pkv, kind):
+    """Scores that rise along the keys, by more than 2^8 between the halves of
+    a step and between steps: every rescale is taken."""
+    def kv(k, v):
+        t = torch.arange(k.shape[0], dtype=torch.float32)
+        return k * 0.01 + (t // 64)[:, None, None] * 0.35, v
+
+    p = Problem(pkv, kind, 128, 16, 4, 1, [400], [200], seed=3, kv=kv)
+    p.q = p.q.abs() * 0.5
+    for o in ({}, dict(softcap=400.0)):
+        want, vmax = p.expected(**o)
+        p.check(p.run(**o), want, vmax, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bs", [8, 32])
+def test_tiles_leave_out_bad_and_freed_blocks(pkv, kind, bs):
+    lens, rows, W = [500, 200], [60, 70], 90
+    p = Problem(pkv, kind, 128, bs, 8, 2, lens, rows, seed=5)
+    tables = p.tables.clone()
+    tables[0, 1:(500 - 60 - W) // bs] = -9       # before every row's window, past the sinks
+    want = p.expected(window=W, sinks=3)
+    p.check(p.run(tables=tables, window=W, sinks=3), *want, kind)
+    assert pkv.get_device_error() == 0
+    tables = p.tables.clone()
+    tables[1, 2] = p.pool
+    got = p.run(tables=tables)
+    assert pkv.get_device_error() == pkv.DEVERR_BAD_BLOCK_ID
+    p.check(got, *p.expected(missing={1: range(2 * bs, 3 * bs)}), kind)
 
 
 @pytest.mark.parametrize("kind", ["int8", "fp4"])
