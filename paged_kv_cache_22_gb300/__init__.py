@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -524,27 +525,33 @@ def copy_blocks(k_dst: torch.Tensor, v_dst: torch.Tensor, k_src: torch.Tensor, v
 
 
 # ------------------------------------------------------------------ quantised caches, modified scores
-@contextlib.contextmanager
-def _launching(stream, *tensors):
-    """The device of the call's tensors made current (they must share one),
-    and the stream the call runs on; allocations inside belong to it."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or not next(iter(devices)).type == "cuda":
-        raise ValueError("tensors must live on one CUDA device")
-    device = next(iter(devices))
-    if stream is not None and stream.device != device:
+# The host side of a small call costs more than its kernels, so these calls
+# look at every tensor once and enter no context manager on the usual path.
+def _device_of(*tensors) -> int:
+    """The index of the one CUDA device that holds the tensors, all contiguous."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None:
+            if t.get_device() != dev or dev < 0:
+                raise ValueError("tensors must live on one CUDA device")
+            if not t.is_contiguous():
+                raise ValueError("tensors must be contiguous")
+    return dev
+
+
+def _on(dev: int, stream, call):
+    """call(stream handle) with the tensors' device current and, for a stream
+    of the caller's, with that stream current too: what the call allocates
+    belongs to the stream it runs on."""
+    if stream is None and torch._C._cuda_getDevice() == dev:
+        return call(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is not None and stream.device_index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-        else:
-            with torch.cuda.stream(stream):
-                yield ctypes.c_void_p(stream.cuda_stream)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return call(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _int(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, numel: Optional[int] = None) -> None:
-    if t is None:
-        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {str(dtype)[6:]}")
     if numel is not None and t.numel() != numel:
@@ -558,6 +565,7 @@ def _format(fmt: str) -> int:
         raise ValueError(f"unknown quantised format {fmt!r}: one of {', '.join(QUANT_FORMATS)}") from None
 
 
+@functools.lru_cache(maxsize=None)
 def quant_tile_bytes(head_dim: int, block_size: int, fmt: str) -> int:
     """Bytes of one (block, kv head) tile of a quantised cache."""
     n = int(library().pkv_quant_tile_bytes(head_dim, block_size, _format(fmt)))
@@ -573,12 +581,22 @@ def quant_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_
 
 def _quant_desc(k_cache: torch.Tensor, v_cache: torch.Tensor, block_size: int, head_dim: int, fmt: str) -> QuantDesc:
     tile = quant_tile_bytes(head_dim, block_size, fmt)
-    for c in (k_cache, v_cache):
-        if c.dtype != torch.uint8 or c.dim() != 3 or c.shape[2] != tile:
-            raise ValueError(f"quantised caches are uint8 [num_blocks, num_kv_heads, {tile}]")
-    if k_cache.shape != v_cache.shape:
+    shape = k_cache.shape
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or len(shape) != 3 or shape[2] != tile:
+        raise ValueError(f"quantised caches are uint8 [num_blocks, num_kv_heads, {tile}]")
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    return QuantDesc(k_cache.shape[0], block_size, k_cache.shape[1], head_dim, _format(fmt))
+    return QuantDesc(shape[0], block_size, shape[1], head_dim, QUANT_FORMATS[fmt])
+
+
+def _tables(block_tables: torch.Tensor, seq_lens: torch.Tensor):
+    """(sequences, table entries per sequence) after the checks of both."""
+    _int("block_tables", block_tables, torch.int32)
+    _int("seq_lens", seq_lens, torch.int32)
+    B, shape = seq_lens.numel(), block_tables.shape
+    if len(shape) != 2 or shape[0] != B:
+        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    return B, shape[1]
 
 
 def kv_quantize_and_cache(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -590,18 +608,21 @@ def kv_quantize_and_cache(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tenso
     e4m3 scale per 16 elements and one scale per (token, kv head).  The scales
     come from the rows themselves.  A row with an infinity or a NaN reads back
     as NaN."""
-    if k.dtype not in (torch.float32, torch.bfloat16) or v.dtype != k.dtype:
+    dtype, shape = k.dtype, k.shape
+    if dtype not in (torch.float32, torch.bfloat16) or v.dtype != dtype:
         raise TypeError("k and v must both be float32 or bfloat16")
-    if k.dim() != 3 or v.shape != k.shape:
+    if len(shape) != 3 or v.shape != shape:
         raise ValueError("k and v are [num_tokens, num_kv_heads, head_dim]")
-    _int("slot_mapping", slot_mapping, torch.int64, k.shape[0])
-    desc = _quant_desc(k_cache, v_cache, block_size, int(k.shape[2]), fmt)
-    if desc.num_kv_heads != k.shape[1]:
-        raise ValueError(f"the cache has {desc.num_kv_heads} kv heads, k has {k.shape[1]}")
-    with _launching(stream, k, v, k_cache, v_cache, slot_mapping) as st:
-        _check(library().pkv_kv_quantize_and_cache(
-            _ptr(k), _ptr(v), _dt(k), int(k.shape[0]), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc),
-            _ptr(slot_mapping), st), "kv_quantize_and_cache")
+    T, Hkv, d = shape
+    _int("slot_mapping", slot_mapping, torch.int64, T)
+    desc = _quant_desc(k_cache, v_cache, block_size, d, fmt)
+    if desc.num_kv_heads != Hkv:
+        raise ValueError(f"the cache has {desc.num_kv_heads} kv heads, k has {Hkv}")
+    dev = _device_of(k, v, k_cache, v_cache, slot_mapping)
+    call = library().pkv_kv_quantize_and_cache
+    _check(_on(dev, stream, lambda st: call(
+        k.data_ptr(), v.data_ptr(), _CACHE_DT[dtype], T, k_cache.data_ptr(), v_cache.data_ptr(), ctypes.byref(desc),
+        slot_mapping.data_ptr(), st)), "kv_quantize_and_cache")
 
 
 def gather_kv_quant(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
@@ -613,71 +634,79 @@ def gather_kv_quant(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: 
     ``total_tokens`` they are read from ``seq_lens`` (with a synchronisation)."""
     if out_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("out_dtype must be float32 or bfloat16")
-    B = seq_lens.numel()
-    _int("block_tables", block_tables, torch.int32)
-    _int("seq_lens", seq_lens, torch.int32)
-    _int("cu_seq_lens", cu_seq_lens, torch.int64, B + 1)
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
+    B, mbps = _tables(block_tables, seq_lens)
+    if cu_seq_lens is not None:
+        _int("cu_seq_lens", cu_seq_lens, torch.int64, B + 1)
     desc = _quant_desc(k_cache, v_cache, block_size, head_dim, fmt)
-    with _launching(stream, k_cache, v_cache, block_tables, seq_lens, cu_seq_lens) as st:
-        if cu_seq_lens is None:
-            cu_seq_lens = torch.zeros(B + 1, dtype=torch.int64, device=seq_lens.device)
-            cu_seq_lens[1:] = torch.cumsum(seq_lens.to(torch.int64), 0)
-        if total_tokens is None:
-            total_tokens = int(cu_seq_lens[-1].item())
-        k_out = torch.empty((total_tokens, desc.num_kv_heads, head_dim), dtype=out_dtype, device=k_cache.device)
-        v_out = torch.empty_like(k_out)
-        _check(library().pkv_gather_kv_quant(
-            _ptr(k_out), _ptr(v_out), _dt(k_out), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc),
-            _ptr(block_tables), int(block_tables.shape[1]), _ptr(seq_lens), _ptr(cu_seq_lens), B, total_tokens,
-            int(max_seq_len), st), "gather_kv_quant")
-    return k_out, v_out
+    dev = _device_of(k_cache, v_cache, block_tables, seq_lens, cu_seq_lens)
+    call = library().pkv_gather_kv_quant
+
+    def run(st):
+        cu, total = cu_seq_lens, total_tokens
+        if cu is None:
+            cu = torch.zeros(B + 1, dtype=torch.int64, device=seq_lens.device)
+            cu[1:] = torch.cumsum(seq_lens.to(torch.int64), 0)
+        if total is None:
+            total = int(cu[-1].item())
+        shape = (total, desc.num_kv_heads, head_dim)
+        k_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+        v_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+        _check(call(k_out.data_ptr(), v_out.data_ptr(), _CACHE_DT[out_dtype], k_cache.data_ptr(), v_cache.data_ptr(),
+                    ctypes.byref(desc), block_tables.data_ptr(), mbps, seq_lens.data_ptr(), cu.data_ptr(), B, total,
+                    max_seq_len, st), "gather_kv_quant")
+        return k_out, v_out
+
+    return _on(dev, stream, run)
 
 
 def scored_workspace_bytes(num_seqs: int, max_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
     """Workspace of :func:`paged_attention_scored` and :func:`paged_attention_quant`
-    (``max_q`` 1 for one query token per sequence)."""
+    on the current device (``max_q`` 1 for one query token per sequence)."""
     return int(library().pkv_scored_workspace_bytes(num_seqs, max_q, num_q_heads, num_kv_heads, head_dim))
 
 
 def _attend(call, what, desc, kv_scale, out, q, k_cache, v_cache, block_tables, seq_lens, scale, q_start, max_q, softcap,
             alibi_slopes, window, sinks, prefix_lens, max_seq_len, workspace, stream):
-    if q.dim() != 3 or out.shape != q.shape or out.dtype != q.dtype:
+    shape = q.shape
+    if len(shape) != 3 or out.shape != shape or out.dtype != q.dtype:
         raise ValueError("q and out are [rows, num_q_heads, head_dim] of one type")
-    total, Hq, d = q.shape
+    total, Hq, d = shape
     if d != desc.head_dim:
         raise ValueError(f"q has head_dim {d}, the cache {desc.head_dim}")
-    B = seq_lens.numel()
-    _int("block_tables", block_tables, torch.int32)
-    _int("seq_lens", seq_lens, torch.int32)
-    _int("q_start", q_start, torch.int32, B + 1)
-    _int("prefix_lens", prefix_lens, torch.int32, B)
-    _int("alibi_slopes", alibi_slopes, torch.float32, Hq)
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables must be [num_seqs, max_blocks_per_seq]")
-    if q_start is None and total != B:
+    B, mbps = _tables(block_tables, seq_lens)
+    slopes = prefixes = starts = None
+    if q_start is not None:
+        _int("q_start", q_start, torch.int32, B + 1)
+        starts = q_start.data_ptr()
+    elif total != B:
         raise ValueError("q must have one row per sequence (or q_start given)")
-    mbps = int(block_tables.shape[1])
+    if prefix_lens is not None:
+        _int("prefix_lens", prefix_lens, torch.int32, B)
+        prefixes = prefix_lens.data_ptr()
+    if alibi_slopes is not None:
+        _int("alibi_slopes", alibi_slopes, torch.float32, Hq)
+        slopes = alibi_slopes.data_ptr()
     if max_seq_len is None:
         max_seq_len = mbps * desc.block_size
-    with _launching(stream, out, q, k_cache, v_cache, block_tables, seq_lens, q_start, alibi_slopes, prefix_lens) as st:
-        if q_start is None:
-            max_q = 1
-        elif max_q is None:
-            max_q = int((q_start[1:] - q_start[:-1]).max().item()) if B else 0
-        opts = ScoreOpts(float(softcap), _ptr(alibi_slopes), _ptr(prefix_lens), int(window), int(sinks))
-        nbytes = scored_workspace_bytes(B, max_q, Hq, desc.num_kv_heads, d)
+    dev = _device_of(q, out, k_cache, v_cache, block_tables, seq_lens, q_start, alibi_slopes, prefix_lens)
+    opts = ScoreOpts(softcap, slopes, prefixes, window, sinks)
+
+    def run(st):
+        rows = 1 if q_start is None else max_q
+        if rows is None:
+            rows = int((q_start[1:] - q_start[:-1]).max().item()) if B else 0
+        nbytes = scored_workspace_bytes(B, rows, Hq, desc.num_kv_heads, d)
         # without a workspace of the caller's the call has one of its own: calls
         # on several streams and captured graphs then share nothing
-        ws = (torch.empty(max(nbytes, 256), dtype=torch.uint8, device=q.device) if workspace is None
+        ws = (torch.empty(nbytes, dtype=torch.uint8, device=q.device) if workspace is None
               else workspace.get(nbytes))
-        qdt = F32 if q.dtype == torch.float32 else _dt(q)
-        args = [_ptr(out), _ptr(q), qdt, _ptr(q_start), B, total, int(max_q), Hq, _ptr(k_cache), _ptr(v_cache),
-                ctypes.byref(desc), _ptr(block_tables), mbps, _ptr(seq_lens), int(max_seq_len), float(scale)]
+        args = (out.data_ptr(), q.data_ptr(), _dt(q), starts, B, total, rows, Hq, k_cache.data_ptr(), v_cache.data_ptr(),
+                ctypes.byref(desc), block_tables.data_ptr(), mbps, seq_lens.data_ptr(), max_seq_len, scale)
         if kv_scale is not None:
-            args.append(float(kv_scale))
-        _check(call(*args, ctypes.byref(opts), _ptr(ws), ws.numel(), st), what)
+            args += (kv_scale,)
+        return call(*args, ctypes.byref(opts), ws.data_ptr(), ws.numel(), st)
+
+    _check(_on(dev, stream, run), what)
     return out
 
 
@@ -713,7 +742,7 @@ def paged_attention_quant(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Ten
                           stream=None) -> torch.Tensor:
     """:func:`paged_attention_scored` over a quantised cache
     (:func:`kv_quantize_and_cache`; ``block_size`` and ``fmt`` as there)."""
-    desc = _quant_desc(k_cache, v_cache, block_size, int(q.shape[-1]), fmt)
+    desc = _quant_desc(k_cache, v_cache, block_size, q.shape[-1], fmt)
     return _attend(library().pkv_paged_attention_quant, "paged_attention_quant", desc, None, out, q, k_cache, v_cache,
                    block_tables, seq_lens, scale, q_start, max_q, softcap, alibi_slopes, window, sinks, prefix_lens,
                    max_seq_len, workspace, stream)

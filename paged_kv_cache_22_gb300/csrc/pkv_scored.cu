@@ -25,6 +25,9 @@ int column_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 // Query rows of a (sequence, kv head) from which a call takes the 128-row tiles.
 constexpr int64_t kTileRows = 128;
+bool takes_tiles(bool several, int64_t rows, int num_seqs, int num_kv_heads) {
+  return several && rows >= kTileRows && num_seqs <= 65535 && num_kv_heads <= 65535;
+}
 
 // CTAs per SM the workspace is sized for.
 int max_ctas_per_sm(int nt) { return nt == 1 ? 16 : 8; }
@@ -132,7 +135,7 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounters);
 
   TmaMaps maps{};
-  if (q_start && rows >= kTileRows && num_seqs <= 65535 && desc.num_kv_heads <= 65535) {
+  if (takes_tiles(q_start && max_q > 1, rows, num_seqs, desc.num_kv_heads)) {
     const tiles::Kernel t = pick_tile_kernel(kind, D, bs);
     if (prepare(t.fn, tiles::kThreads, t.smem, dev) <= 0) return PKV_ERR_CUDA;
     if ((kind == cols::kBf16 || kind == cols::kFp8) && !encode_operand_maps(&desc, k_cache, v_cache, &maps))
@@ -184,7 +187,9 @@ size_t pkv_scored_workspace_bytes(int32_t num_seqs, int32_t max_q, int32_t num_q
     return 0;
   const int sms = pkv_device_sm_count();
   if (sms <= 0) return 0;
-  const int nt = column_tiles((int64_t)max_q * (num_q_heads / num_kv_heads));
+  const int64_t rows = (int64_t)max_q * (num_q_heads / num_kv_heads);
+  if (takes_tiles(max_q > 1, rows, num_seqs, num_kv_heads)) return kCounters;  // nothing is cut
+  const int nt = column_tiles(rows);
   return kCounters + (size_t)2 * sms * max_ctas_per_sm(nt) * cols::slot_floats(8 * nt, head_dim) * sizeof(float);
 }
 

@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRun = 16;  // elements per thread
+constexpr int kTokens = 16;  // tokens of a head that consecutive rows of threads write
 
 struct QuantWriteArgs {
   unsigned int* err;
@@ -43,36 +44,62 @@ struct QuantGatherArgs {
   int len_clip;
 };
 
-// 16 consecutive elements as binary32, from 16-byte aligned memory read once.
-__device__ __forceinline__ void load_run(const float* p, float (&x)[kRun]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + i);
-    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+// 32 bytes of global memory in one access where the address allows it, past
+// L1 (two accesses of 16 bytes touch half of a sector each).
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
 }
-__device__ __forceinline__ void load_run(const __nv_bfloat16* p, float (&x)[kRun]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = bf16x2_to_f2(w[k]);
-      x[8 * i + 2 * k] = f.x;
-      x[8 * i + 2 * k + 1] = f.y;
-    }
-  }
+// Streaming stores of 16 bytes: L2 joins the halves of a sector.  (One store
+// of 32 bytes measured 263 us against 243 for the read-back of 262144 x 8 fp4
+// rows, 268 against 271 for int8.)
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  __stcs(static_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+  __stcs(static_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
 }
 
-// The largest magnitude as its bits: the bits of magnitudes order as the
-// magnitudes do, infinity and then NaN above every finite one.
-__device__ __forceinline__ uint32_t run_max(const float (&x)[kRun]) {
-  uint32_t m = 0;
+// A run of 16 consecutive elements, held as it came (8 registers for bf16) and
+// widened where it is used.
+template <class Src>
+struct Run;
+template <>
+struct Run<float> {
+  uint32_t w[2][8];
+  __device__ __forceinline__ void load(const float* p) {
+    load32(p, w[0]);
+    load32(p + 8, w[1]);
+  }
+  __device__ __forceinline__ float operator[](int i) const { return __uint_as_float(w[i / 8][i % 8]); }
+  // The largest magnitude as its bits: the bits of magnitudes order as the
+  // magnitudes do, infinity and then NaN above every finite one.
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kRun; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  return m;
-}
+    for (int i = 0; i < kRun; ++i) m = max(m, w[i / 8][i % 8] & 0x7FFFFFFFu);
+    return m;
+  }
+};
+template <>
+struct Run<__nv_bfloat16> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { load32(p, w); }
+  __device__ __forceinline__ float operator[](int i) const {
+    return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+  __device__ __forceinline__ uint32_t max_bits() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);  // both halves of a word at once
+    return max(m << 16, m & 0xFFFF0000u);
+  }
+};
 
 // Two binary32 values -> two e2m1 codes (lo in bits 0..3), to nearest even,
 // saturating.
@@ -81,92 +108,138 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
   return r;
 }
+__device__ __forceinline__ uint32_t e2m1x8(const float* y) {
+  return e2m1x2(y[0], y[1]) | e2m1x2(y[2], y[3]) << 8 | e2m1x2(y[4], y[5]) << 16 | e2m1x2(y[6], y[7]) << 24;
+}
 
-// Four codes of 8 bits from four whole numbers -128..127 held as
-// 0x4B400000 + n (a float whose unit is 1): the low bytes, plus 128.
-__device__ __forceinline__ uint32_t pack4(const float* n) {
-  uint32_t w = 0;
+// The codes are those of the binary32 quotient x / s.  A division costs about
+// ten instructions, more than everything else a run needs, and a product with
+// the reciprocal differs from it in the last place only: it is used wherever
+// that cannot change the code, that is, away from the borders between codes.
+// One run in a few thousand takes the division.
+
+// 1.5 * 2^23 + 128: a float whose unit is 1, with the biased code in its low byte.
+constexpr float kMagic = 12583040.f;
+
+template <class R>
+__device__ __forceinline__ void int8_codes(const R& x, float s, uint32_t (&w)[4]) {
+  const float inv = __frcp_rn(s);
+  // |x / s| <= 127 (1 + 2^-23), so that the quotient and the product are
+  // within 2^-16 of each other.  (Ties are not rare: with bf16 elements
+  // 127 x / a is a ratio of small whole numbers.)
+  constexpr float kNear = 0.5f - 0x1p-15f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= ((__float_as_uint(n[i]) + 128u) & 0xFFu) << (8 * i);
-  return w;
+  for (int k = 0; k < 4; ++k) {
+    float n[4], d[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float2 v = make_float2(x[4 * k + i], x[4 * k + i + 1]), c = make_float2(kMagic, kMagic);
+      const float2 r = ffma2(v, make_float2(inv, inv), c);  // rounds x * inv to a whole number, ties to even
+      const float2 e = ffma2(v, make_float2(inv, inv), ffma2(r, make_float2(-1.f, -1.f), c));
+      n[i] = r.x; n[i + 1] = r.y;
+      d[i] = e.x; d[i + 1] = e.y;
+    }
+    if (fmaxf(fmaxf(fabsf(d[0]), fabsf(d[1])), fmaxf(fabsf(d[2]), fabsf(d[3]))) > kNear) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (fabsf(d[i]) > kNear) n[i] = __fadd_rn(rintf(__fdiv_rn(x[4 * k + i], s)), kMagic);
+    }
+    const uint32_t lo = __byte_perm(__float_as_uint(n[0]), __float_as_uint(n[1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(n[2]), __float_as_uint(n[3]), 0x0040);
+    w[k] = __byte_perm(lo, hi, 0x5410);
+  }
+}
+
+template <class R>
+__device__ __forceinline__ void fp4_codes(const R& x, float step, uint32_t (&w)[2]) {
+  // codes do not fall as the quotient grows: where a product a little below it
+  // and one a little above (2^-21 either way) agree, it has that code too
+  const float inv = __frcp_rn(step), lo = inv * (1.f - 0x1p-21f), hi = inv * (1.f + 0x1p-21f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[8], z[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 v = make_float2(x[8 * h + i], x[8 * h + i + 1]);
+      const float2 a = __fmul2_rn(v, make_float2(lo, lo)), b = __fmul2_rn(v, make_float2(hi, hi));
+      y[i] = a.x; y[i + 1] = a.y;
+      z[i] = b.x; z[i + 1] = b.y;
+    }
+    w[h] = e2m1x8(y);
+    const uint32_t diff = w[h] ^ e2m1x8(z);
+    if (diff) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // the pair of byte i
+        if (diff >> (8 * i) & 0xFFu)
+          w[h] = (w[h] & ~(0xFFu << (8 * i))) |
+                 e2m1x2(__fdiv_rn(x[8 * h + 2 * i], step), __fdiv_rn(x[8 * h + 2 * i + 1], step)) << (8 * i);
+    }
+  }
 }
 
 // One run of a row, quantised into its tile: codes, group scale, row scale.
-template <int D, int BS, bool FP4>
-__device__ __forceinline__ void store_run(const float (&x)[kRun], uint32_t row_max, uint32_t run_m, int seg, int off,
+template <int D, int BS, bool FP4, class R>
+__device__ __forceinline__ void store_run(const R& x, uint32_t row_max, uint32_t run_m, int seg, int off,
                                           uint8_t* tile) {
   constexpr int ROW = quant_row_bytes(D, FP4);
   const bool bad = row_max >= 0x7F800000u;  // an infinity or a NaN in the row
   const float amax = __uint_as_float(row_max);
   const bool zero = bad || amax < kQuantTiny;
-  float* scales = reinterpret_cast<float*>(tile + BS * (ROW + quant_group_bytes(D, FP4)));
+  const float s = zero ? 0.f : __fdiv_rn(amax, FP4 ? 2688.f : 127.f);
   if constexpr (!FP4) {
-    const float s = zero ? 0.f : __fdiv_rn(amax, 127.f);
     uint32_t w[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
-    if (!zero) {
-      float n[kRun];
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) n[i] = __fadd_rn(rintf(__fdiv_rn(x[i], s)), 12582912.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack4(n + 4 * i);
-    }
+    if (!zero) int8_codes(x, s, w);
     *reinterpret_cast<uint4*>(tile + off * ROW + 16 * quant_chunk(off, seg, ROW)) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (seg == 0) scales[off] = bad ? __uint_as_float(0x7FC00000u) : s;
   } else {
-    const float s = zero ? 0.f : __fdiv_rn(amax, 2688.f);
     uint32_t w[2] = {0u, 0u}, t = 0;
     if (!zero) {
       t = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(run_m), __fmul_rn(6.f, s)), __NV_SATFINITE, __NV_E4M3);
       __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)t, __NV_E4M3);
       const float step = __fmul_rn(__half2float(*reinterpret_cast<__half*>(&hr)), s);
-      if (step > 0.f) {
-#pragma unroll
-        for (int i = 0; i < kRun / 2; ++i)
-          w[i / 4] |= e2m1x2(__fdiv_rn(x[2 * i], step), __fdiv_rn(x[2 * i + 1], step)) << (8 * (i % 4));
-      }
+      if (step > 0.f) fp4_codes(x, step, w);
     }
     *reinterpret_cast<uint2*>(tile + off * ROW + 16 * quant_chunk(off, seg / 2, ROW) + 8 * (seg % 2)) =
         make_uint2(w[0], w[1]);
     tile[BS * ROW + off * (D / 16) + seg] = (uint8_t)t;
-    if (seg == 0) scales[off] = bad ? __uint_as_float(0x7FC00000u) : s;
   }
+  if (seg == 0)
+    reinterpret_cast<float*>(tile + BS * (ROW + quant_group_bytes(D, FP4)))[off] = bad ? __uint_as_float(0x7FC00000u) : s;
 }
 
 // One thread per run: the K and the V run of the same (token, head, segment).
 template <class Src, int D, int BS, bool FP4>
-__global__ void __launch_bounds__(kThreads) kv_quantize_kernel(const __grid_constant__ QuantWriteArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(Src) == 4 ? 3 : 5) kv_quantize_kernel(const __grid_constant__ QuantWriteArgs a) {
   constexpr int SEGS = D / kRun, TILE = quant_tile_bytes(D, BS, FP4);
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t row = i / SEGS;
-  const int seg = (int)(i % SEGS);
-  const int64_t rows = (int64_t)a.num_tokens * a.num_kv_heads;
-  // a row's threads are SEGS consecutive lanes and end together; lanes past
-  // the last row stay for the shuffles
+  // Consecutive rows of threads are consecutive tokens of one head, kTokens at
+  // a time: neighbours in a prompt are neighbours in a tile, so that a warp's
+  // row scales (and an fp4 tile's group scales) are one access, not one each.
+  constexpr uint32_t GROUP = kTokens * SEGS, PER_CTA = kThreads / GROUP;  // threads of a head's tokens
+  const int seg = threadIdx.x % SEGS;
+  const uint32_t hh = blockIdx.x * PER_CTA + threadIdx.x / GROUP;
+  const uint32_t tg = hh / (uint32_t)a.num_kv_heads;
+  const int h = (int)(hh - tg * (uint32_t)a.num_kv_heads);
+  const int64_t t = (int64_t)tg * kTokens + threadIdx.x % GROUP / SEGS;
+  const int64_t row = t * a.num_kv_heads + h;
+  // a row's threads are SEGS consecutive lanes and end together; lanes without
+  // a token stay for the shuffles
+  const bool have = t < a.num_tokens;
   int64_t slot = -1;
-  int h = 0;
-  if (row < rows) {
-    const int t = (int)(row / a.num_kv_heads);
-    h = (int)(row % a.num_kv_heads);
+  if (have) {
     slot = __ldg(a.slot_mapping + t);
     if (slot >= a.num_slots) {
       raise_error(a.err, PKV_DEVERR_BAD_SLOT);
       slot = -1;
     }
   }
-  float x[2][kRun];
+  Run<Src> x[2] = {};
   uint32_t m[2], rm[2];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    if (slot >= 0) {
-      load_run(reinterpret_cast<const Src*>(c ? a.v : a.k) + row * D + seg * kRun, x[c]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kRun; ++e) x[c][e] = 0.f;
-    }
+  if (have) {  // (a skipped token's row is read too: the loads do not wait for the slot)
+    x[0].load(reinterpret_cast<const Src*>(a.k) + row * D + seg * kRun);
+    x[1].load(reinterpret_cast<const Src*>(a.v) + row * D + seg * kRun);
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    m[c] = run_max(x[c]);
+    m[c] = x[c].max_bits();
     rm[c] = m[c];
 #pragma unroll
     for (int o = SEGS / 2; o > 0; o >>= 1) rm[c] = max(rm[c], __shfl_xor_sync(0xffffffffu, rm[c], o));
@@ -180,8 +253,12 @@ __global__ void __launch_bounds__(kThreads) kv_quantize_kernel(const __grid_cons
 
 __device__ __forceinline__ void store_vals(float* p, const float (&x)[kRun]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    __stcs(reinterpret_cast<float4*>(p) + i, make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]));
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(x[8 * i + k]);
+    store32(p + 8 * i, w);
+  }
 }
 __device__ __forceinline__ void store_vals(__nv_bfloat16* p, const float (&x)[kRun]) {
   uint32_t w[8];
@@ -190,8 +267,7 @@ __device__ __forceinline__ void store_vals(__nv_bfloat16* p, const float (&x)[kR
     const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
-  __stcs(reinterpret_cast<uint4*>(p) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+  store32(p, w);
 }
 
 // The 16 values of segment `seg` of row `off` of a tile.
@@ -203,20 +279,27 @@ __device__ __forceinline__ void load_vals(const uint8_t* tile, int off, int seg,
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(tile + off * ROW + 16 * quant_chunk(off, seg, ROW)));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) x[i] = __fmul_rn((float)((int)(w[i / 4] >> (8 * (i % 4)) & 0xFFu) - 128), s);
+    for (int i = 0; i < kRun; ++i)  // 2^23 + byte, less 2^23 + 128: the code
+      x[i] = __fmul_rn(__uint_as_float(__byte_perm(w[i / 4], 0x4B000000u, 0x7540 + i % 4)) - 8388736.f, s);
   } else {
     const uint2 v = __ldg(reinterpret_cast<const uint2*>(tile + off * ROW + 16 * quant_chunk(off, seg / 2, ROW) + 8 * (seg % 2)));
     const uint32_t tc = __ldg(tile + BS * ROW + off * (D / 16) + seg);
-    __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)tc, __NV_E4M3);
-    const float t = __half2float(*reinterpret_cast<__half*>(&hr));
+    const __half2_raw tr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(tc | tc << 8), __NV_E4M3);
     const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const uint32_t c = w[i / 8] >> (4 * (i % 8));
-      // e2m1 bits as the top bits of a binary16 exponent and mantissa: the
-      // value times 2^-14, subnormals included
-      const __half_raw raw{(unsigned short)((c & 7u) << 9 | (c & 8u) << 12)};
-      x[i] = __fmul_rn(__half2float(*reinterpret_cast<const __half*>(&raw)) * 16384.f * t, s);
+    for (int i = 0; i < 2; ++i) {
+      uint32_t f[4];
+      asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+          : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+          : "r"(w[i]));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // code * group scale is exact in binary16 (six bits)
+        const float2 y = __half22float2(__hmul2(*reinterpret_cast<const __half2*>(&f[k]), *reinterpret_cast<const __half2*>(&tr)));
+        x[8 * i + 2 * k] = __fmul_rn(y.x, s);
+        x[8 * i + 2 * k + 1] = __fmul_rn(y.y, s);
+      }
     }
   }
 }
@@ -303,7 +386,8 @@ pkv_status pkv_kv_quantize_and_cache(const void* k, const void* v, pkv_dtype src
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
       (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
     return PKV_ERR_INVALID_ARG;
-  const int64_t threads = (int64_t)num_tokens * cache->num_kv_heads * (cache->head_dim / kRun);
+  const int64_t threads =
+      ((int64_t)num_tokens + kTokens - 1) / kTokens * kTokens * cache->num_kv_heads * (cache->head_dim / kRun);
   const int64_t ctas = (threads + kThreads - 1) / kThreads;
   if (ctas > 0x7FFFFFFF) return PKV_ERR_UNSUPPORTED;
   unsigned int* err = current_error_word();
