@@ -37,10 +37,10 @@
 //    the B operand by one 8x8 transpose (movmatrix) per 8 tokens.
 //  * Row scales of a quantised cache never touch the codes.  K's multiplies
 //    the score.  V's multiplies the probability before it is rounded to fp16:
-//    w = 2^((z - m) + log2(s_v)) with m a running maximum of z + log2(s_v),
-//    so that the largest weight, not the largest probability, sits near one
-//    and scales of any size keep 11 bits; the sum of the probabilities
-//    2^(z - m) is kept in fp32 relative to the same m.
+//    w = 2^(z + log2(s_v) - m) with m a running maximum of z + log2(s_v), so
+//    that the largest weight, not the largest probability, sits near one and
+//    scales of any size keep 11 bits; the sum takes the probability w / s_v,
+//    in fp32.
 //  * bf16 caches: P is a bf16 head plus a bf16 remainder (16 bits, two MMAs);
 //    fp8 and quantised caches: one fp16 operand (11 bits).  A weight rounded
 //    to 11 bits moves an output by at most 2^-12 max|V|, an eighth of the
@@ -87,20 +87,26 @@ struct Geo {
   static constexpr int ROW = KIND == kBf16 ? 2 * D : (KIND == kFp4 ? D / 2 : D);
   static constexpr int IB = ROW >= 128 ? 128 : ROW;  // bytes of a swizzled line part
   static constexpr int CPB = IB / 16;
-  static constexpr int BPT = BS < 16 ? 16 / BS : 1;  // blocks per tile
+  // Tokens per tile: 32 for codes (two independent products per step of the
+  // loop, and its fixed costs spread over twice the tokens), 16 for bf16, whose
+  // tiles are two to four times larger (HBM sets the pace there).
+  static constexpr int WANT = KIND == kBf16 ? 16 : 32;
+  static constexpr int BPT = BS < WANT ? WANT / BS : 1;  // blocks per tile
   static constexpr int TOK = BS * BPT;               // tokens per tile
-  static constexpr int STEPS = TOK / 16;
+  static constexpr int STEPS = TOK / 16;             // m16 rows of tokens per tile
+  static constexpr int NI = 2 * STEPS;               // tokens of a tile per lane
   static constexpr int BLOCK = REC ? quant_tile_bytes(D, BS, KIND == kFp4) : BS * ROW;  // one block's bytes of K or V
   static constexpr int CACHE = BPT * BLOCK;
   static constexpr int STAGE = 2 * CACHE;            // K then V
   static constexpr int KS = D / 16;                  // k-steps of q.K
   static constexpr int MT = D / 16;                  // m-tiles of V^T P^T
+  static constexpr int STEP = BS == 32 ? 16 * IB : 16 / BS * BLOCK;  // bytes from a step's rows to the next's
   static constexpr int DPL = D / 4;                  // codes: dims of a K row per lane
   static constexpr int DL = D / 8;                   // codes: dims of a V row per lane
-  // stages per warp: about 14 KiB in flight, at least two
-  static constexpr int N0 = 14336 / STAGE;
+  // stages per warp: about 16 KiB in flight, at least two
+  static constexpr int N0 = 17408 / STAGE;
   static constexpr int NS = N0 < 2 ? 2 : (N0 > 6 ? 6 : N0);
-  static_assert(REC || STAGE % 1024 == 0 || BS * IB % 512 == 0, "tensor copies keep the swizzle phase");
+  static_assert(REC || STAGE % 1024 == 0, "tensor copies keep the swizzle phase");
 };
 
 __host__ __device__ constexpr int slot_floats(int NC, int D) { return NC * D + 2 * NC; }
@@ -175,34 +181,46 @@ __device__ __forceinline__ Chunk chunk_of(const Args& a, int v) {
   return c;
 }
 
+// The stream's T tiles over N warps: the first T % N warps take one more.
+// Counts are 32-bit (the host refuses a call whose bound passes 2^31 tiles).
+struct Split {
+  uint32_t T, per, rem;
+  __device__ __forceinline__ Split(uint32_t t, uint32_t n) : T(t), per(t / n), rem(t - t / n * n) {}
+  __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * per + min(w, rem); }
+  __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+    const uint32_t cut = rem * (per + 1);
+    return u < cut ? u / (per + 1) : rem + (u - cut) / per;
+  }
+};
+
 // Walk over the (chunk, kv head) segments of a range of the tile stream.
 struct Walk {
   int v, h;        // chunk index over all sequences, kv head
   Chunk c;
   int nb;          // tiles of the segment
-  int64_t base;    // first tile of chunk v in the stream
+  uint32_t base;   // first tile of chunk v in the stream
   int jb, je;      // piece = tiles [jb, je) of the segment
   bool done;
-  __device__ __forceinline__ int64_t seg() const { return base + (int64_t)h * nb; }
+  __device__ __forceinline__ uint32_t seg() const { return base + (uint32_t)h * nb; }
 };
 
 template <int NC, int TOK>
-__device__ __forceinline__ void settle(Walk& w, const Args& a, int64_t u1) {
+__device__ __forceinline__ void settle(Walk& w, const Args& a, uint32_t u1) {
   const int vs = a.num_seqs * a.chunks;
   while (!w.done) {
     if (w.nb > 0 && w.h < a.num_kv_heads) {
-      const int64_t left = u1 - w.seg();
+      const int left = (int)(u1 - w.seg());
       if (left <= 0) {
         w.done = true;
         return;
       }
-      w.je = left < w.nb ? (int)left : w.nb;
+      w.je = min(left, w.nb);
       if (w.jb < w.je) return;
       w.jb = 0;
       ++w.h;
       continue;
     }
-    w.base += (int64_t)w.nb * a.num_kv_heads;
+    w.base += (uint32_t)w.nb * a.num_kv_heads;
     w.h = 0;
     w.jb = 0;
     if (++w.v >= vs || w.base >= u1) {
@@ -215,7 +233,7 @@ __device__ __forceinline__ void settle(Walk& w, const Args& a, int64_t u1) {
 }
 
 template <int NC, int TOK>
-__device__ __forceinline__ void next_piece(Walk& w, const Args& a, int64_t u1) {
+__device__ __forceinline__ void next_piece(Walk& w, const Args& a, uint32_t u1) {
   if (w.je < w.nb) {  // the range ended inside this segment
     w.done = true;
     return;
@@ -225,54 +243,55 @@ __device__ __forceinline__ void next_piece(Walk& w, const Args& a, int64_t u1) {
   settle<NC, TOK>(w, a, u1);
 }
 
-// The range [u0, u1) of the tile stream of warp gw of NW (T tiles in all) and
-// the walk on its first piece; false when the warp has none.
+// Tiles of the whole stream (every lane of a warp).
 template <int NC, int TOK>
-__device__ __forceinline__ bool plan(const Args& a, int64_t gw, int64_t NW, int lane, Walk& w, int64_t& u0,
-                                     int64_t& u1, int64_t& T) {
+__device__ __forceinline__ uint32_t total_tiles(const Args& a, int lane) {
   const int vs = a.num_seqs * a.chunks;
-  int64_t mine = 0;
+  uint32_t mine = 0;
   for (int v = lane; v < vs; v += 32) mine += chunk_of<NC, TOK>(a, v).tiles();
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  T = mine * a.num_kv_heads;
-  u0 = range_start(gw, T, NW);
-  u1 = range_start(gw + 1, T, NW);
-  if (u0 >= u1) return false;
-  int64_t run = 0;
+  return __reduce_add_sync(0xffffffffu, mine) * a.num_kv_heads;
+}
+
+// The walk on the first piece of the range [u0, u1), u0 < u1.
+template <int NC, int TOK>
+__device__ __forceinline__ Walk walk_from(const Args& a, uint32_t u0, uint32_t u1, int lane) {
+  Walk w;
+  w.done = true;
+  const int vs = a.num_seqs * a.chunks;
+  uint32_t run = 0;
   for (int v = 0; v < vs; v += 32) {
-    const int64_t n = v + lane < vs ? (int64_t)chunk_of<NC, TOK>(a, v + lane).tiles() * a.num_kv_heads : 0;
-    int64_t incl = n;
+    const uint32_t n = v + lane < vs ? (uint32_t)chunk_of<NC, TOK>(a, v + lane).tiles() * a.num_kv_heads : 0;
+    uint32_t incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, incl, o);
+      const uint32_t t = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += t;
     }
-    const int64_t excl = run + incl - n;
-    const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && excl <= u0 && u0 < excl + n);
+    const uint32_t excl = run + incl - n;
+    const unsigned hit = __ballot_sync(0xffffffffu, excl <= u0 && u0 < excl + n);
     if (hit) {
       const int src = __ffs(hit) - 1;
       w.v = v + src;
       w.base = __shfl_sync(0xffffffffu, excl, src);
       w.c = chunk_of<NC, TOK>(a, w.v);
       w.nb = w.c.tiles();
-      const int64_t off = u0 - w.base;
-      w.h = (int)(off / w.nb);
-      w.jb = (int)(off % w.nb);
+      const uint32_t off = u0 - w.base;
+      w.h = (int)(off / (uint32_t)w.nb);
+      w.jb = (int)(off - (uint32_t)w.h * w.nb);
       w.done = false;
       settle<NC, TOK>(w, a, u1);
-      return true;
+      return w;
     }
     run += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return false;
+  return w;
 }
 
 // The partial slot of a cut piece: two per warp, the first for a piece that
 // starts the warp's range, the second for a later one.
 template <int NC, int D>
-__device__ __forceinline__ float* slot_of(const Args& a, const Walk& w, int64_t gw, int64_t u0) {
-  const int64_t k = w.seg() + w.jb == u0 ? 2 * gw : 2 * gw + 1;
+__device__ __forceinline__ float* slot_of(const Args& a, const Walk& w, uint32_t gw, uint32_t u0) {
+  const uint32_t k = w.seg() + w.jb == u0 ? 2 * gw : 2 * gw + 1;
   return a.partials + (size_t)k * slot_floats(NC, D);
 }
 
@@ -375,18 +394,19 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
   }
   __syncwarp();
 
-  const int64_t gw = blockIdx.x, NW = gridDim.x;
+  const uint32_t gw = blockIdx.x, NW = gridDim.x;
   // decode rows of empty sequences are zero
   if (!a.q_start) {
-    for (int64_t s = gw; s < a.num_seqs; s += NW) {
+    for (uint32_t s = gw; s < (uint32_t)a.num_seqs; s += NW) {
       if (__ldg(a.seq_lens + s) > 0 && a.len_clip > 0) continue;
-      uint4* o = reinterpret_cast<uint4*>(a.out + s * a.num_q_heads * D);
+      uint4* o = reinterpret_cast<uint4*>(a.out + (size_t)s * a.num_q_heads * D);
       for (int i = lane; i < a.num_q_heads * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
     }
   }
-  int64_t u0 = 0, u1 = 0, T = 0;
-  Walk wk;
-  if (!plan<NC, TOK>(a, gw, NW, lane, wk, u0, u1, T)) return;
+  const Split split(total_tiles<NC, TOK>(a, lane), NW);
+  const uint32_t u0 = split.start(gw), u1 = split.start(gw + 1);
+  if (u0 >= u1) return;
+  Walk wk = walk_from<NC, TOK>(a, u0, u1, lane);
 
   // ---------------------------------------------------------------- issue side
   Walk cw = wk;
@@ -394,11 +414,14 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
   // id of block b of the j-th tile of the walk's segment; kNoBlock where a tile
   // of two blocks has one that no row attends (its entry may hold anything)
   constexpr int32_t kNoBlock = INT32_MIN;
+  const int32_t* table = nullptr;
+  auto table_of = [&](const Walk& w) { return a.block_tables + (size_t)(a.chunks > 1 ? w.v / a.chunks : w.v) * a.table_stride; };
   auto block_id = [&](const Walk& w, int j, int b) -> int32_t {
     const int e = w.c.tile(j) * GE::BPT + b;
     if (GE::BPT > 1 && e * BS >= w.c.a_max && (e * BS >= w.c.hi_max || (e + 1) * BS <= w.c.lo_min)) return kNoBlock;
-    return __ldg(a.block_tables + (w.v / a.chunks) * a.table_stride + e);
+    return __ldg(table + e);
   };
+  table = table_of(cw);
   int32_t next_id[GE::BPT];
 #pragma unroll
   for (int b = 0; b < GE::BPT; ++b) next_id[b] = block_id(cw, cj, b);
@@ -439,6 +462,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
     if (++cj >= cw.je) {
       next_piece<NC, TOK>(cw, a, u1);
       cj = cw.jb;
+      if (!cw.done) table = table_of(cw);
     }
     if (!cw.done) {
 #pragma unroll
@@ -588,18 +612,18 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
         if (!(blocks >> b & 1)) there &= ~(low_bits(BS) << (b * (BS & 31)));
       const bool inner = there == low_bits(TOK) && tb >= all_lo && tb + TOK <= all_hi;
 
+      // ---- S^T = K Q^T per step of 16 tokens; two chains of k-steps where
+      // there is one step
+      constexpr int STEPS = GE::STEPS, CH = STEPS == 1 ? 2 : 1, NI = GE::NI;
+      const uint8_t* stage = smem + st * GE::STAGE;
+      float s2[STEPS][CH][NT][4];
 #pragma unroll
-      for (int step = 0; step < GE::STEPS; ++step) {
-        const uint8_t* kt = smem + st * GE::STAGE + step * 16 * GE::IB;
-        const uint8_t* vt = kt + GE::CACHE;
-        // (bf16 rows of two spans: chunk_at adds the span's offset)
-
-        // ---- S^T = K Q^T, two chains of k-steps
-        float s2[2][NT][4];
+      for (int step = 0; step < STEPS; ++step) {
+        const uint8_t* kt = stage + step * GE::STEP;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < CH; ++c)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) s2[c][n][0] = s2[c][n][1] = s2[c][n][2] = s2[c][n][3] = 0.f;
+          for (int n = 0; n < NT; ++n) s2[step][c][n][0] = s2[step][c][n][1] = s2[step][c][n][2] = s2[step][c][n][3] = 0.f;
         if constexpr (BF) {
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
@@ -607,7 +631,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
             ldsm_x4(smem_addr(kt + chunk_at(kr, 2 * k + kc)), r);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              mma_k16_rows16<false>(s2[k & 1][n], r[0], r[1], r[2], r[3], qb[n][k][0], qb[n][k][1]);
+              mma_k16_rows16<false>(s2[step][k % CH][n], r[0], r[1], r[2], r[3], qb[n][k][0], qb[n][k][1]);
           }
         } else {
           constexpr int CB = KIND == kFp4 ? GE::DPL / 2 : GE::DPL;  // code bytes of a row per lane: 8, 16 or 32
@@ -631,8 +655,8 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
             uint32_t gs[2][GPL];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int r = g + 8 * i, rr = r + 16 * step;
-              const uint8_t* p = smem + st * GE::STAGE + (rr / BS) * GE::BLOCK + BS * GE::ROW + (rr % BS) * (D / 16) + GPL * t;
+              const int rr = g + 8 * i + 16 * step;
+              const uint8_t* p = stage + (rr / BS) * GE::BLOCK + BS * GE::ROW + (rr % BS) * (D / 16) + GPL * t;
               uint32_t two = GPL == 2 ? *reinterpret_cast<const uint16_t*>(p) : (uint32_t)*p;
 #pragma unroll
               for (int q = 0; q < GPL; ++q) gs[i][q] = e4m3x2_to_f16x2(__byte_perm(two, 0, q ? 0x4411 : 0x4400));
@@ -651,8 +675,8 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
               for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
-                  mma_k16_rows16<true>(s2[h][n], f0[2 * h], f1[2 * h], f0[2 * h + 1], f1[2 * h + 1], qb[n][2 * w + h][0],
-                                       qb[n][2 * w + h][1]);
+                  mma_k16_rows16<true>(s2[step][h % CH][n], f0[2 * h], f1[2 * h], f0[2 * h + 1], f1[2 * h + 1],
+                                       qb[n][2 * w + h][0], qb[n][2 * w + h][1]);
             }
           } else {
 #pragma unroll
@@ -667,113 +691,120 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
               }
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma_k16_rows16<true>(s2[k & 1][n], a0, a1, a2, a3, qb[n][k][0], qb[n][k][1]);
+                mma_k16_rows16<true>(s2[step][k % CH][n], a0, a1, a2, a3, qb[n][k][0], qb[n][k][1]);
             }
           }
         }
+      }
 
-        // ---- scores of tokens g, g + 8: z (base 2), and z + log2 of V's row scale
-        float ksc[2] = {1.f, 1.f}, vlg[2] = {0.f, 0.f};
-        if constexpr (REC) {
+      // ---- scores of tokens g + 8 i: z (base 2), log2 of V's row scale, its inverse
+      float ksc[NI], vlg[NI], vis[NI];
+      if constexpr (REC) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int rr = g + 8 * i + 16 * step;
-            const uint8_t* p = smem + st * GE::STAGE + (rr / BS) * GE::BLOCK + GE::BLOCK - 4 * BS + 4 * (rr % BS);
-            ksc[i] = *reinterpret_cast<const float*>(p);
-            const float lg = fast_log2(*reinterpret_cast<const float*>(p + GE::CACHE));
-            vlg[i] = lg < kMinLogScale ? kMinLogScale : lg;  // (a NaN scale stays NaN)
+        for (int i = 0; i < NI; ++i) {
+          const int rr = g + 8 * i;
+          const uint8_t* p = stage + (rr / BS) * GE::BLOCK + GE::BLOCK - 4 * BS + 4 * (rr % BS);
+          ksc[i] = *reinterpret_cast<const float*>(p);
+          const float lg = fast_log2(*reinterpret_cast<const float*>(p + GE::CACHE));
+          vlg[i] = lg < kMinLogScale ? kMinLogScale : lg;  // (a NaN scale stays NaN)
+          vis[i] = fast_exp2(-vlg[i]);
+        }
+      }
+      float z[NI][NE];
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float (&sc)[CH][NT][4] = s2[i / 2];
+            const int k = 2 * (i % 2) + e;
+            float x = (CH == 2 ? sc[0][n][k] + sc[CH - 1][n][k] : sc[0][n][k]) * qmul[2 * n + e];
+            if constexpr (REC) x *= ksc[i];
+            z[i][2 * n + e] = x;
           }
+      if (a.cap > 0.f) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int c = 0; c < NE; ++c) z[i][c] = soft_cap(z[i][c], a.cap, a.inv_cap);
+      }
+      if (a.slopes) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float pos = (float)(tb + g + 8 * i);
+#pragma unroll
+          for (int c = 0; c < NE; ++c) z[i][c] = fmaf(-slope[c], fabsf(col_pos[c] - pos), z[i][c]);
         }
-        float z[2][NE];
-        bool grow = false;
+      }
+      if constexpr (REC) {  // z + log2(s_v): what the weight is a power of
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int c = 0; c < NE; ++c) z[i][c] += vlg[i];
+      }
+      if (!inner) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = (s2[0][n][2 * i + e] + s2[1][n][2 * i + e]) * qmul[2 * n + e];
-              if constexpr (REC) x *= ksc[i];
-              z[i][2 * n + e] = x;
-            }
-        if (a.cap > 0.f) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < NE; ++c) z[i][c] = soft_cap(z[i][c], a.cap, a.inv_cap);
-        }
-        const int tok0 = 16 * step + g;
-        if (a.slopes) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float pos = (float)(tb + tok0 + 8 * i);
-#pragma unroll
-            for (int c = 0; c < NE; ++c) z[i][c] = fmaf(-slope[c], fabsf(col_pos[c] - pos), z[i][c]);
-          }
-        }
-        float lg[2][NE];  // log2 of V's row scale; 0 at a masked position, whose scale may be NaN
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < NE; ++c) lg[i][c] = vlg[i];
-        if (!inner) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int tk = tok0 + 8 * i, pos = tb + tk;
-#pragma unroll
-            for (int c = 0; c < NE; ++c) {
-              const bool keep = (there >> tk & 1) && (pos < col_a[c] || (pos >= col_lo[c] && pos < col_hi[c]));
-              z[i][c] = keep ? z[i][c] : -CUDART_INF_F;
-              lg[i][c] = keep ? vlg[i] : 0.f;
-            }
-          }
-        }
-        float zw[2][NE];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < NI; ++i) {
+          const int tk = g + 8 * i, pos = tb + tk;
 #pragma unroll
           for (int c = 0; c < NE; ++c) {
-            zw[i][c] = REC ? z[i][c] + lg[i][c] : z[i][c];
-            grow = grow || zw[i][c] > m[c] + kSlack;
+            const bool keep = (there >> tk & 1) && (pos < col_a[c] || (pos >= col_lo[c] && pos < col_hi[c]));
+            z[i][c] = keep ? z[i][c] : -CUDART_INF_F;
           }
-        if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-          for (int c = 0; c < NE; ++c) {
-            float mx = fmaxf(zw[0][c], zw[1][c]);
-#pragma unroll
-            for (int sh = 4; sh <= 16; sh <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, sh));
-            const float mn = fmaxf(m[c], mx);
-            const float alpha = mn > m[c] ? fast_exp2(m[c] - mn) : 1.f;
-            m[c] = mn;
-            l[c] *= alpha;
-#pragma unroll
-            for (int jm = 0; jm < MT; ++jm) {
-              o[c / 2][jm][c % 2] *= alpha;
-              o[c / 2][jm][2 + c % 2] *= alpha;
-            }
-          }
+          if constexpr (REC) vis[i] = vis[i] < CUDART_INF_F ? vis[i] : 1.f;  // beside a masked scale that is no number
         }
-        float wgt[2][NE];
+      }
+      bool grow = false;
+      float mx[NE];
+#pragma unroll
+      for (int c = 0; c < NE; ++c) {
+        mx[c] = z[0][c];
+#pragma unroll
+        for (int i = 1; i < NI; ++i) mx[c] = fmaxf(mx[c], z[i][c]);
+        grow = grow || mx[c] > m[c] + kSlack;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int c = 0; c < NE; ++c) {
-          const float mu = m[c] == -CUDART_INF_F ? 0.f : m[c];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // the weight and the probability share the rounded difference, so
-            // that their ratio is the scale even where z is large
-            const float d = z[i][c] - mu;
-            wgt[i][c] = fast_exp2(REC ? d + lg[i][c] : d);
-            l[c] += REC ? fast_exp2(d) : wgt[i][c];
+          for (int sh = 4; sh <= 16; sh <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], sh));
+          const float mn = fmaxf(m[c], mx[c]);
+          const float alpha = mn > m[c] ? fast_exp2(m[c] - mn) : 1.f;
+          m[c] = mn;
+          l[c] *= alpha;
+#pragma unroll
+          for (int jm = 0; jm < MT; ++jm) {
+            o[c / 2][jm][c % 2] *= alpha;
+            o[c / 2][jm][2 + c % 2] *= alpha;
           }
         }
+      }
+#pragma unroll
+      for (int c = 0; c < NE; ++c) {
+        const float mu = m[c] == -CUDART_INF_F ? 0.f : m[c];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          z[i][c] = fast_exp2(z[i][c] - mu);  // the weight; the probability is the weight / s_v
+          l[c] = REC ? fmaf(z[i][c], vis[i], l[c]) : l[c] + z[i][c];
+        }
+      }
 
+      // rows of V that no column attends may hold anything: they become zero
+      // (0 * NaN is NaN)
+      uint32_t vkeep = 0xFFFFFFFFu;  // bit k: token k of the tile
+      if (!inner) vkeep = there & (low_bits(wk.c.a_max - tb) | (low_bits(any_hi - tb) & ~low_bits(any_lo - tb)));
+
+#pragma unroll
+      for (int step = 0; step < STEPS; ++step) {
+        const uint8_t* vt = stage + GE::CACHE + step * GE::STEP;
         // ---- P^T as the B operand: columns = query rows, k = tokens
         uint32_t pb[NT][2], pr[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float w0 = wgt[i][2 * n], w1 = wgt[i][2 * n + 1];
+            const float w0 = z[2 * step + i][2 * n], w1 = z[2 * step + i][2 * n + 1];
             const uint32_t h = BF ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
             pb[n][i] = movmatrix_t(h);
             if constexpr (BF) {
@@ -782,13 +813,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
             }
           }
 
-        // ---- O^T += V^T P^T; rows of V that no column attends may hold
-        // anything: they become zero (0 * NaN is NaN)
-        uint32_t vkeep = 0xFFFFFFFFu;  // bit k: token k of the tile
-        if (!inner) {
-          const uint32_t some = low_bits(wk.c.a_max - tb) | (low_bits(any_hi - tb) & ~low_bits(any_lo - tb));
-          vkeep = there & some;
-        }
+        // ---- O^T += V^T P^T
         auto kept = [&](int tk) -> bool { return vkeep >> (16 * step + tk) & 1; };
         if constexpr (BF) {
           const uint32_t k0 = (kept(2 * t) ? 0xFFFFu : 0u) | (kept(2 * t + 1) ? 0xFFFF0000u : 0u);
@@ -822,7 +847,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
               X[i][0] = *reinterpret_cast<const uint32_t*>(p);
             }
             const int rr = tk[i] + 16 * step;
-            sc[i] = smem[st * GE::STAGE + GE::CACHE + (rr / BS) * GE::BLOCK + BS * GE::ROW + (rr % BS) * (D / 16) + g * GE::DL / 16];
+            sc[i] = stage[GE::CACHE + (rr / BS) * GE::BLOCK + BS * GE::ROW + (rr % BS) * (D / 16) + g * GE::DL / 16];
             if (!inner && !kept(tk[i])) sc[i] = 0u;  // an unwritten scale may be NaN
           }
           gv[0] = e4m3x2_to_f16x2(sc[0] | sc[1] << 8);
@@ -982,26 +1007,41 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
 constexpr int kMergeWarps = 4;
 
 template <int D, int TOK, int NT>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_cols_kernel(const __grid_constant__ Args a, int64_t NW) {
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_cols_kernel(const __grid_constant__ Args a, uint32_t NW) {
   constexpr int NC = 8 * NT, SLOT = slot_floats(NC, D), V = D / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t gw = blockIdx.x;
-  int64_t u0 = 0, u1 = 0, T = 0;
-  Walk w;
-  const bool mine = plan<NC, TOK>(a, gw, NW, lane, w, u0, u1, T) && w.jb > 0 && w.seg() + w.nb <= u1;
+  const uint32_t gw = blockIdx.x;
+  __shared__ Walk plan;
+  if (warp == 0) {
+    const Split split(total_tiles<NC, TOK>(a, lane), NW);
+    const uint32_t u0 = split.start(gw), u1 = split.start(gw + 1);
+    Walk w;
+    w.done = true;
+    if (u0 < u1) {
+      w = walk_from<NC, TOK>(a, u0, u1, lane);
+      if (!w.done && (w.jb == 0 || w.seg() + w.nb > u1)) w.done = true;
+      if (!w.done) {
+        // the segment's parts: `jb` becomes their number, `je` the first one's slot
+        const uint32_t first = split.owner(w.seg());
+        w.jb = (int)(gw - first + 1);
+        w.je = (int)(w.seg() != split.start(first) ? 2 * first + 1 : 2 * first);
+      }
+    }
+    if (lane == 0) plan = w;
+  }
+  __syncthreads();
+  const Walk w = plan;
   // CTA 0 waits in any case, so that this grid never completes before the
   // attention grid it depends on
-  if (mine || gw == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!mine) return;
-  const int64_t seg = w.seg();
-  const int64_t first = owner_of(seg, T, NW);
-  const int64_t n = gw - first + 1;
-  const int64_t slot0 = seg != range_start(first, T, NW) ? 2 * first + 1 : 2 * first;
-  auto part = [&](int64_t i) -> const float* { return a.partials + (size_t)(i == 0 ? slot0 : 2 * (first + i)) * SLOT; };
+  if (!w.done || gw == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (w.done) return;
+  const int n = w.jb;
+  const uint32_t slot0 = (uint32_t)w.je, first = gw + 1 - n;
+  auto part = [&](int i) -> const float* { return a.partials + (size_t)(i == 0 ? slot0 : 2 * (first + i)) * SLOT; };
   const int rows = w.c.T * a.group;
   for (int col = warp; col < NC && w.c.r0 + col < rows; col += kMergeWarps) {
     float M = -CUDART_INF_F;
-    for (int64_t i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + NC * D + col));
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + NC * D + col));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (M == -CUDART_INF_F) M = 0.f;
@@ -1009,7 +1049,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_cols_kernel(const __gr
 #pragma unroll
     for (int d = 0; d < V; ++d) num[d] = 0.f;
 #pragma unroll 4
-    for (int64_t i = 0; i < n; ++i) {
+    for (int i = 0; i < n; ++i) {
       const float* p = part(i);
       const float f = fast_exp2(__ldcg(p + NC * D + col) - M);
       den = fmaf(f, __ldcg(p + NC * D + NC + col), den);

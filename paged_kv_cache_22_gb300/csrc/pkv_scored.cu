@@ -156,6 +156,7 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   // one wave of warps, no more than there are tiles
   int64_t grid = (int64_t)sms * std::min(occ, max_ctas_per_sm(nt));
   const int64_t tiles = num_seqs * chunks * desc.num_kv_heads * ((a.len_clip + k.tok - 1) / k.tok);
+  if (tiles >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;  // the kernels count them in 32 bits
   grid = std::max<int64_t>(1, std::min(grid, tiles));
   void* args[] = {&a, &maps};
   if (cudaLaunchKernel(k.fn, dim3((unsigned)grid), dim3(32), args, k.smem, st) != cudaSuccess) return PKV_ERR_CUDA;
@@ -169,7 +170,8 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void* margs[] = {&a, &grid};
+  uint32_t warps = (uint32_t)grid;
+  void* margs[] = {&a, &warps};
   return cudaLaunchKernelExC(&cfg, k.merge, margs) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
