@@ -51,6 +51,8 @@
 
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "decode_tc.cuh"
 #include "quant_layout.cuh"
 
@@ -79,6 +81,16 @@ struct Args {
   const int32_t* prefix_lens;
   int window, sinks;
   float* partials;  // [2 * CTAs][slot_floats(NC, D)]
+  struct Cut* cuts; // [CTAs]
+};
+
+// A segment cut between warps, described by the warp that ends it (parts 0: none).
+struct Cut {
+  int parts;              // pieces of the segment, on consecutive warps
+  uint32_t slot0, first;  // partial slot of the first piece; its warp
+  int row0;               // first query row of q / out of the chunk's sequence
+  int r0, rows, head0;    // first row of the chunk, rows of the (sequence, kv head), first query head
+  int pad;
 };
 
 template <int KIND, int D, int BS>
@@ -100,26 +112,20 @@ struct Geo {
   static constexpr int STAGE = 2 * CACHE;            // K then V
   static constexpr int KS = D / 16;                  // k-steps of q.K
   static constexpr int MT = D / 16;                  // m-tiles of V^T P^T
-  static constexpr int STEP = BS == 32 ? 16 * IB : 16 / BS * BLOCK;  // bytes from a step's rows to the next's
+  // bytes from a token's code row, group scales and row scale to those of the
+  // token 8 rows on, and 16 rows on (the next step)
+  static constexpr int R8 = BS == 8 ? BLOCK : 8 * IB, R16 = BS == 32 ? 16 * IB : 16 / BS * BLOCK;
+  static constexpr int G8 = BS == 8 ? BLOCK : D / 2, G16 = BS == 32 ? D : 16 / BS * BLOCK;
+  static constexpr int S8 = BS == 8 ? BLOCK : 32, S16 = BS == 32 ? 64 : 16 / BS * BLOCK;
   static constexpr int DPL = D / 4;                  // codes: dims of a K row per lane
   static constexpr int DL = D / 8;                   // codes: dims of a V row per lane
-  // stages per warp: about 16 KiB in flight, at least two
-  static constexpr int N0 = 17408 / STAGE;
-  static constexpr int NS = N0 < 2 ? 2 : (N0 > 6 ? 6 : N0);
+  // Stages per warp: two (four of the smallest): the other warps of the SM keep
+  // the copies going, and shared memory decides how many those are.
+  static constexpr int NS = STAGE <= 2560 ? 4 : 2;
   static_assert(REC || STAGE % 1024 == 0, "tensor copies keep the swizzle phase");
 };
 
 __host__ __device__ constexpr int slot_floats(int NC, int D) { return NC * D + 2 * NC; }
-
-template <int KIND, int D, int BS, int NT>
-struct Smem {
-  using GE = Geo<KIND, D, BS>;
-  static constexpr int kStages = 0;
-  static constexpr int kQ = GE::NS * GE::STAGE;                   // [2][NC][D] bf16
-  static constexpr int kBars = (kQ + 2 * 8 * NT * D * 2 + 15) / 16 * 16;
-  static constexpr int kOk = kBars + 8 * GE::NS;                  // bit b: block b of the stage is there
-  static constexpr int kBytes = kOk + 4 * GE::NS;
-};
 
 // A chunk of query rows of a sequence and the tiles its rows attend: tiles
 // [0, na) and [wt, nt) (na == wt when nothing is left out).
@@ -181,6 +187,12 @@ __device__ __forceinline__ Chunk chunk_of(const Args& a, int v) {
   return c;
 }
 
+// What a query row (column) attends: positions [0, a) and [lo, hi).
+struct Col {
+  int a, lo, hi;
+  float slope;  // distance bias, base 2
+};
+
 // The stream's T tiles over N warps: the first T % N warps take one more.
 // Counts are 32-bit (the host refuses a call whose bound passes 2^31 tiles).
 struct Split {
@@ -202,6 +214,22 @@ struct Walk {
   int jb, je;      // piece = tiles [jb, je) of the segment
   bool done;
   __device__ __forceinline__ uint32_t seg() const { return base + (uint32_t)h * nb; }
+};
+
+template <int KIND, int D, int BS, int NT>
+struct Smem {
+  using GE = Geo<KIND, D, BS>;
+  static constexpr int kStages = 0;
+  static constexpr int kQ = GE::NS * GE::STAGE;                   // [NC][D] bf16: the next piece's query rows
+  static constexpr int kBars = (kQ + 8 * NT * D * 2 + 15) / 16 * 16;
+  static constexpr int kOk = kBars + 8 * GE::NS;                  // bit b: block b of the stage is there
+  static constexpr int kWalks = (kOk + 4 * GE::NS + 15) / 16 * 16;  // this piece's, the next one's, the copies'
+  static constexpr int kCols = kWalks + 3 * (int)sizeof(Walk);    // [NC] column limits
+  static constexpr int kBytes = kCols + 8 * NT * (int)sizeof(Col);
+  // CTAs per SM that shared memory allows (1 KiB of it per CTA is the
+  // system's), at most 16: the register budget follows
+  static constexpr int kFit = 233472 / (kBytes + 1024);
+  static constexpr int kCtas = NT == 2 ? 8 : (kFit > 16 ? 16 : kFit);
 };
 
 template <int NC, int TOK>
@@ -355,6 +383,32 @@ __device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap) {
   return cap * (fabsf(u) < 0.25f ? small : big);
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
@@ -368,11 +422,11 @@ constexpr float kSlack = 8.f;  // a score may pass the running maximum by this (
 // The kernel: one warp per CTA.
 // ----------------------------------------------------------------------------
 template <int KIND, int D, int BS, int NT>
-__global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
+__global__ void __launch_bounds__(32, Smem<KIND, D, BS, NT>::kCtas)
     attn_cols_kernel(const __grid_constant__ Args a, const __grid_constant__ TmaMaps maps) {
   using GE = Geo<KIND, D, BS>;
   using SM = Smem<KIND, D, BS, NT>;
-  constexpr int NC = 8 * NT, TOK = GE::TOK, NS = GE::NS, KS = GE::KS, MT = GE::MT, NE = 2 * NT;
+  constexpr int NC = 8 * NT, TOK = GE::TOK, NS = GE::NS, KS = GE::KS, MT = GE::MT;
   constexpr bool REC = GE::REC, BF = KIND == kBf16;
   extern __shared__ __align__(1024) uint8_t cols_smem[];
   uint8_t* const smem = cols_smem;
@@ -405,28 +459,56 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
   }
   const Split split(total_tiles<NC, TOK>(a, lane), NW);
   const uint32_t u0 = split.start(gw), u1 = split.start(gw + 1);
-  if (u0 >= u1) return;
-  Walk wk = walk_from<NC, TOK>(a, u0, u1, lane);
+  if (u0 >= u1) {
+    if (lane == 0) a.cuts[gw].parts = 0;
+    return;
+  }
+  // The walks live in shared memory (every lane would hold the same words of
+  // them in registers): [0] and [1] the piece in work and the next, [2] the
+  // piece being copied.
+  Walk* const walks = reinterpret_cast<Walk*>(smem + SM::kWalks);
+  Col* const col_s = reinterpret_cast<Col*>(smem + SM::kCols);
+  {
+    const Walk w = walk_from<NC, TOK>(a, u0, u1, lane);
+    if (lane == 0) {
+      walks[0] = walks[2] = w;
+      // a range that starts inside a segment and reaches its end: this warp
+      // leaves the merge grid the segment's description
+      Cut c{};
+      if (w.jb > 0 && w.seg() + w.nb <= u1) {
+        c.first = split.owner(w.seg());
+        c.parts = (int)(gw - c.first + 1);
+        c.slot0 = w.seg() != split.start(c.first) ? 2 * c.first + 1 : 2 * c.first;
+        c.row0 = w.c.q0;
+        c.r0 = w.c.r0;
+        c.rows = w.c.T * a.group;
+        c.head0 = w.h * a.group;
+      }
+      a.cuts[gw] = c;
+    }
+  }
+  __syncwarp();
 
   // ---------------------------------------------------------------- issue side
-  Walk cw = wk;
-  int cj = wk.jb, issued = 0;
+  const Walk& cw = walks[2];
+  int cj = cw.jb, issued = 0;
+  bool more = true;  // tiles left to copy
   // id of block b of the j-th tile of the walk's segment; kNoBlock where a tile
-  // of two blocks has one that no row attends (its entry may hold anything)
+  // of several blocks has one that no row attends (its entry may hold anything)
   constexpr int32_t kNoBlock = INT32_MIN;
-  const int32_t* table = nullptr;
-  auto table_of = [&](const Walk& w) { return a.block_tables + (size_t)(a.chunks > 1 ? w.v / a.chunks : w.v) * a.table_stride; };
-  auto block_id = [&](const Walk& w, int j, int b) -> int32_t {
-    const int e = w.c.tile(j) * GE::BPT + b;
-    if (GE::BPT > 1 && e * BS >= w.c.a_max && (e * BS >= w.c.hi_max || (e + 1) * BS <= w.c.lo_min)) return kNoBlock;
+  const int32_t* table;
+  auto set_table = [&]() { table = a.block_tables + (size_t)(a.chunks > 1 ? cw.v / a.chunks : cw.v) * a.table_stride; };
+  auto block_id = [&](int j, int b) -> int32_t {
+    const int e = cw.c.tile(j) * GE::BPT + b;
+    if (GE::BPT > 1 && e * BS >= cw.c.a_max && (e * BS >= cw.c.hi_max || (e + 1) * BS <= cw.c.lo_min)) return kNoBlock;
     return __ldg(table + e);
   };
-  table = table_of(cw);
+  set_table();
   int32_t next_id[GE::BPT];
 #pragma unroll
-  for (int b = 0; b < GE::BPT; ++b) next_id[b] = block_id(cw, cj, b);
+  for (int b = 0; b < GE::BPT; ++b) next_id[b] = block_id(cj, b);
   auto issue_next = [&]() {
-    if (cw.done) return;
+    if (!more) return;
     const int st = issued % NS;
     uint8_t* dst = smem + st * GE::STAGE;
     uint32_t ok = 0;
@@ -434,6 +516,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
     for (int b = 0; b < GE::BPT; ++b)
       if (next_id[b] >= 0 && next_id[b] < a.num_blocks) ok |= 1u << b;
     if (elect_one()) {
+      const int h = cw.h;
 #pragma unroll
       for (int b = 0; b < GE::BPT; ++b)
         if (!(ok >> b & 1) && next_id[b] != kNoBlock) raise_error(a.err, PKV_DEVERR_BAD_BLOCK_ID);
@@ -445,45 +528,50 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
         uint8_t* kd = dst + b * GE::BLOCK;
         uint8_t* vd = kd + GE::CACHE;
         if constexpr (REC) {
-          const size_t off = ((size_t)next_id[b] * a.num_kv_heads + cw.h) * GE::BLOCK;
+          const size_t off = ((size_t)next_id[b] * a.num_kv_heads + h) * GE::BLOCK;
           bulk_g2s(kd, a.k_cache + off, GE::BLOCK, &bars[st]);
           bulk_g2s(vd, a.v_cache + off, GE::BLOCK, &bars[st]);
         } else if constexpr (GE::ROW > GE::IB) {
-          tma_load_4d(kd, &maps.k, 0, cw.h * BS, 0, next_id[b], &bars[st]);
-          tma_load_4d(vd, &maps.v, 0, cw.h * BS, 0, next_id[b], &bars[st]);
+          tma_load_4d(kd, &maps.k, 0, h * BS, 0, next_id[b], &bars[st]);
+          tma_load_4d(vd, &maps.v, 0, h * BS, 0, next_id[b], &bars[st]);
         } else {
-          tma_load_3d(kd, &maps.k, 0, cw.h * BS, next_id[b], &bars[st]);
-          tma_load_3d(vd, &maps.v, 0, cw.h * BS, next_id[b], &bars[st]);
+          tma_load_3d(kd, &maps.k, 0, h * BS, next_id[b], &bars[st]);
+          tma_load_3d(vd, &maps.v, 0, h * BS, next_id[b], &bars[st]);
         }
       }
     }
     __syncwarp();
     ++issued;
     if (++cj >= cw.je) {
-      next_piece<NC, TOK>(cw, a, u1);
-      cj = cw.jb;
-      if (!cw.done) table = table_of(cw);
+      Walk w = cw;
+      next_piece<NC, TOK>(w, a, u1);
+      __syncwarp();
+      if (lane == 0) walks[2] = w;
+      __syncwarp();
+      cj = w.jb;
+      more = !w.done;
+      if (more) set_table();
     }
-    if (!cw.done) {
+    if (more) {
 #pragma unroll
-      for (int b = 0; b < GE::BPT; ++b) next_id[b] = block_id(cw, cj, b);
+      for (int b = 0; b < GE::BPT; ++b) next_id[b] = block_id(cj, b);
     }
   };
-  // the query rows of a chunk into buffer `slot` (16 bytes per lane and copy)
-  auto issue_q = [&](const Walk& w, int slot) {
+  // the query rows of a chunk (16 bytes per lane and copy)
+  auto issue_q = [&](const Walk& w) {
     const int rows = w.c.T * a.group;
 #pragma unroll
     for (int i = lane; i < NC * (D / 8); i += 32) {
       const int col = i / (D / 8), r = w.c.r0 + col;
       if (r < rows) {
         const int64_t row = ((int64_t)w.c.q0 + r / a.group) * a.num_q_heads + w.h * a.group + r % a.group;
-        cp_async16(smem + SM::kQ + ((slot * NC + col) * (D / 8) + i % (D / 8)) * 16, a.q + row * D + (i % (D / 8)) * 8);
+        cp_async16(smem + SM::kQ + (col * (D / 8) + i % (D / 8)) * 16, a.q + row * D + (i % (D / 8)) * 8);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
-  issue_q(wk, 0);
+  issue_q(walks[0]);
 #pragma unroll 1
   for (int i = 0; i < NS; ++i) issue_next();
 
@@ -494,26 +582,39 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
     return (uint32_t)((r / BS) * GE::BLOCK + (c / GE::CPB) * (BS * GE::IB) + rb * GE::IB +
                       (((c % GE::CPB) ^ ((rb * GE::IB / 128) & (GE::CPB - 1))) << 4));
   };
-  // bf16: lane parts of the ldmatrix rows; the chunk's even part is XORed in
-  const int kr = (lane & 7) + 8 * ((lane >> 3) & 1), kc = lane >> 4;
-  const int vr = (lane & 7) + 8 * (lane >> 4), vc = (lane >> 3) & 1;
+  // What a lane reads of a stage, as offsets kept over the whole range; the
+  // rows 8 and 16 further on are constants away (the swizzle repeats).
+  uint32_t kx, vx, vx1 = 0, kg = 0, vg = 0;
+  if constexpr (BF) {
+    // ldmatrix rows; chunk 2k + (lane's half): the even part is XORed in
+    kx = chunk_at((lane & 7) + 8 * ((lane >> 3) & 1), lane >> 4);
+    vx = GE::CACHE + chunk_at((lane & 7) + 8 * (lane >> 4), (lane >> 3) & 1);
+  } else {
+    constexpr int CB = KIND == kFp4 ? GE::DPL / 2 : GE::DPL, VB = KIND == kFp4 ? GE::DL / 2 : GE::DL;
+    kx = chunk_at(g, CB * t / 16) + CB * t % 16;
+    vx = GE::CACHE + chunk_at(2 * t, VB * g / 16) + VB * g % 16;
+    vx1 = GE::CACHE + chunk_at(2 * t + 1, VB * g / 16) + VB * g % 16;
+    if constexpr (KIND == kFp4) {
+      kg = BS * GE::ROW + g * (D / 16) + GE::DPL / 16 * t;
+      vg = GE::CACHE + BS * GE::ROW + 2 * t * (D / 16) + g * GE::DL / 16;
+    }
+  }
+  const uint32_t rx = GE::BLOCK - 4 * BS + 4 * g;  // row scale of token g
 
-  int consumed = 0, waited = 0, piece = 0;
+  int consumed = 0, waited = 0, piece = 0;  // (piece: its walk's slot)
   bool alive = true;
 
 #pragma unroll 1
-  while (!wk.done) {
+  for (bool last = false; !last; ++piece) {
+    const Walk& wk = walks[piece & 1];
     // ---- the piece's query fragments and per-column limits
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();
-    const int qslot = piece & 1;
     const int rows = wk.c.T * a.group;
     uint32_t qb[NT][KS][2];
-    float qmul[NE];
-    int col_a[NE], col_lo[NE], col_hi[NE];
-    float col_pos[NE], slope[NE];
+    float2 qmul[NT];  // score units of columns 2t, 2t + 1
     {
-      const uint8_t* qs = smem + SM::kQ + qslot * NC * D * 2;
+      const uint8_t* qs = smem + SM::kQ;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int col = 8 * n + g;
@@ -525,7 +626,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
             qb[n][k][0] = have ? *reinterpret_cast<const uint32_t*>(qr + (16 * k + 2 * t) * 2) : 0u;
             qb[n][k][1] = have ? *reinterpret_cast<const uint32_t*>(qr + (16 * k + 2 * t + 8) * 2) : 0u;
           }
-          qmul[2 * n] = qmul[2 * n + 1] = a.qk_scale;
+          qmul[n] = make_float2(a.qk_scale, a.qk_scale);
         } else {
           // fp16, each column scaled by a power of two that brings its
           // largest |q| into [2^14, 2^15); the factor goes to the score
@@ -554,48 +655,49 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
               qb[n][k][i] = pack_f16x2(f.x * up, f.y * up);
             }
           }
-          qmul[2 * n] = __shfl_sync(0xffffffffu, down, 8 * t);
-          qmul[2 * n + 1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // rows past the last take the last's limits (their results are dropped)
-          const int i = 2 * n + e, r = min(wk.c.r0 + 8 * n + 2 * t + e, rows - 1);
-          const int hi = wk.c.L - wk.c.T + r / a.group + 1;
-          int pre = a.prefix_lens ? __ldg(a.prefix_lens + wk.v / a.chunks) : 0;
-          pre = min(pre, wk.c.L);
-          col_hi[i] = hi;
-          col_lo[i] = a.window > 0 ? max(0, hi - a.window) : 0;
-          col_a[i] = max(min(a.sinks, hi), pre);
-          col_pos[i] = (float)(hi - 1);
-          slope[i] = a.slopes ? __ldg(a.slopes + wk.h * a.group + r % a.group) * 1.4426950408889634f : 0.f;
+          qmul[n].x = __shfl_sync(0xffffffffu, down, 8 * t);
+          qmul[n].y = __shfl_sync(0xffffffffu, down, 8 * t + 4);
         }
       }
     }
-    // the next piece's query rows while this one runs
-    Walk nx = wk;
-    next_piece<NC, TOK>(nx, a, u1);
-    __syncwarp();
-    if (!nx.done) issue_q(nx, qslot ^ 1);
+    if (lane < NC) {  // rows past the last take the last's limits (their results are dropped)
+      const int r = min(wk.c.r0 + lane, rows - 1);
+      const int hi = wk.c.L - wk.c.T + r / a.group + 1;
+      const int pre = a.prefix_lens ? min(__ldg(a.prefix_lens + wk.v / a.chunks), wk.c.L) : 0;
+      Col c;
+      c.hi = hi;
+      c.lo = a.window > 0 ? max(0, hi - a.window) : 0;
+      c.a = max(min(a.sinks, hi), pre);
+      c.slope = a.slopes ? __ldg(a.slopes + wk.h * a.group + r % a.group) * 1.4426950408889634f : 0.f;
+      col_s[lane] = c;
+    }
+    {  // the next piece's query rows while this one runs
+      Walk nx = wk;
+      next_piece<NC, TOK>(nx, a, u1);
+      last = nx.done;
+      if (lane == 0) walks[(piece + 1) & 1] = nx;
+      __syncwarp();
+      if (!last) issue_q(nx);
+    }
+    const int jb = wk.jb, je = wk.je, L = wk.c.L, na = wk.c.na, gap = wk.c.wt - wk.c.na;
 
     // positions every column attends / some column attends (in the window)
     const int all_lo = a.window > 0 ? max(0, wk.c.hi_max - a.window) : 0, all_hi = wk.c.hi_min;
-    const int any_lo = wk.c.lo_min, any_hi = wk.c.hi_max;
 
     float o[NT][MT][4];
-    float m[NE], l[NE];
+    float2 m[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < MT; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      m[i] = -CUDART_INF_F;
-      l[i] = 0.f;
+    for (int n = 0; n < NT; ++n) {
+      m[n] = make_float2(-CUDART_INF_F, -CUDART_INF_F);
+      l[n] = make_float2(0.f, 0.f);
     }
 
 #pragma unroll 1
-    for (int j = wk.jb; j < wk.je; ++j) {
+    for (int j = jb; j < je; ++j) {
       const int st = consumed % NS;
       bool ok = false;
       if (alive && consumed < issued) {
@@ -603,9 +705,9 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
         waited = consumed + 1;
         if (!ok) alive = false;
       }
-      const int tb = wk.c.tile(j) * TOK;  // first position of the tile
+      const int tb = (j < na ? j : j + gap) * TOK;  // first position of the tile
       // positions of the tile that exist and were copied, one bit each
-      uint32_t there = low_bits(wk.c.L - tb < TOK ? wk.c.L - tb : TOK);
+      uint32_t there = low_bits(L - tb < TOK ? L - tb : TOK);
       const uint32_t blocks = ok ? stage_ok[st] : 0u;
 #pragma unroll
       for (int b = 0; b < GE::BPT; ++b)
@@ -615,11 +717,10 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
       // ---- S^T = K Q^T per step of 16 tokens; two chains of k-steps where
       // there is one step
       constexpr int STEPS = GE::STEPS, CH = STEPS == 1 ? 2 : 1, NI = GE::NI;
-      const uint8_t* stage = smem + st * GE::STAGE;
+      const uint32_t stage = smem_s + st * GE::STAGE;
       float s2[STEPS][CH][NT][4];
 #pragma unroll
       for (int step = 0; step < STEPS; ++step) {
-        const uint8_t* kt = stage + step * GE::STEP;
 #pragma unroll
         for (int c = 0; c < CH; ++c)
 #pragma unroll
@@ -628,7 +729,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             uint32_t r[4];
-            ldsm_x4(smem_addr(kt + chunk_at(kr, 2 * k + kc)), r);
+            ldsm_x4(((stage + kx) ^ (uint32_t)(2 * k % GE::CPB << 4)) + step * GE::R16 + 2 * k / GE::CPB * (BS * GE::IB), r);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
               mma_k16_rows16<false>(s2[step][k % CH][n], r[0], r[1], r[2], r[3], qb[n][k][0], qb[n][k][1]);
@@ -638,15 +739,15 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
           uint32_t kw[2][CB / 4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int r = g + 8 * i;
+            const uint32_t at = stage + kx + step * GE::R16 + i * GE::R8;
             if constexpr (CB >= 16) {
 #pragma unroll
-              for (int c = 0; c < CB / 16; ++c) {
-                const uint4 v = *reinterpret_cast<const uint4*>(kt + chunk_at(r, (CB / 16) * t + c));
+              for (int c = 0; c < CB / 16; ++c) {  // (the lane's second chunk is its first one's neighbour)
+                const uint4 v = lds128(c ? ((stage + step * GE::R16 + i * GE::R8) + (kx ^ 16u)) : at);
                 kw[i][4 * c] = v.x; kw[i][4 * c + 1] = v.y; kw[i][4 * c + 2] = v.z; kw[i][4 * c + 3] = v.w;
               }
             } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(kt + chunk_at(r, t >> 1) + 8 * (t & 1));
+              const uint2 v = lds64(at);
               kw[i][0] = v.x; kw[i][1] = v.y;
             }
           }
@@ -655,11 +756,10 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
             uint32_t gs[2][GPL];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int rr = g + 8 * i + 16 * step;
-              const uint8_t* p = stage + (rr / BS) * GE::BLOCK + BS * GE::ROW + (rr % BS) * (D / 16) + GPL * t;
-              uint32_t two = GPL == 2 ? *reinterpret_cast<const uint16_t*>(p) : (uint32_t)*p;
-#pragma unroll
-              for (int q = 0; q < GPL; ++q) gs[i][q] = e4m3x2_to_f16x2(__byte_perm(two, 0, q ? 0x4411 : 0x4400));
+              const uint32_t at = stage + kg + step * GE::G16 + i * GE::G8;
+              const uint32_t two = e4m3x2_to_f16x2(GPL == 2 ? lds16(at) : lds8(at));
+              gs[i][0] = __byte_perm(two, 0, 0x1010);
+              if constexpr (GPL == 2) gs[i][1] = __byte_perm(two, 0, 0x3232);
             }
 #pragma unroll
             for (int w = 0; w < CB / 4; ++w) {
@@ -697,119 +797,132 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
         }
       }
 
-      // ---- scores of tokens g + 8 i: z (base 2), log2 of V's row scale, its inverse
+      // ---- scores of tokens g + 8 i, column pairs (2t, 2t + 1): z (base 2),
+      // log2 of V's row scale, its inverse
       float ksc[NI], vlg[NI], vis[NI];
       if constexpr (REC) {
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          const int rr = g + 8 * i;
-          const uint8_t* p = stage + (rr / BS) * GE::BLOCK + GE::BLOCK - 4 * BS + 4 * (rr % BS);
-          ksc[i] = *reinterpret_cast<const float*>(p);
-          const float lg = fast_log2(*reinterpret_cast<const float*>(p + GE::CACHE));
+          const uint32_t at = stage + rx + i / 2 * GE::S16 + i % 2 * GE::S8;
+          ksc[i] = __uint_as_float(lds32(at));
+          const float lg = fast_log2(__uint_as_float(lds32(at + GE::CACHE)));
           vlg[i] = lg < kMinLogScale ? kMinLogScale : lg;  // (a NaN scale stays NaN)
           vis[i] = fast_exp2(-vlg[i]);
         }
       }
-      float z[NI][NE];
+      float2 z[NI][NT];
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float (&sc)[CH][NT][4] = s2[i / 2];
-            const int k = 2 * (i % 2) + e;
-            float x = (CH == 2 ? sc[0][n][k] + sc[CH - 1][n][k] : sc[0][n][k]) * qmul[2 * n + e];
-            if constexpr (REC) x *= ksc[i];
-            z[i][2 * n + e] = x;
-          }
+        for (int n = 0; n < NT; ++n) {
+          const int k = 2 * (i % 2);
+          float2 x = make_float2(s2[i / 2][0][n][k], s2[i / 2][0][n][k + 1]);
+          if constexpr (CH == 2) x = __fadd2_rn(x, make_float2(s2[i / 2][CH - 1][n][k], s2[i / 2][CH - 1][n][k + 1]));
+          x = __fmul2_rn(x, qmul[n]);
+          if constexpr (REC) x = __fmul2_rn(x, make_float2(ksc[i], ksc[i]));
+          z[i][n] = x;
+        }
       if (a.cap > 0.f) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int c = 0; c < NE; ++c) z[i][c] = soft_cap(z[i][c], a.cap, a.inv_cap);
+          for (int n = 0; n < NT; ++n)
+            z[i][n] = make_float2(soft_cap(z[i][n].x, a.cap, a.inv_cap), soft_cap(z[i][n].y, a.cap, a.inv_cap));
       }
       if (a.slopes) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const float pos = (float)(tb + g + 8 * i);
+        for (int n = 0; n < NT; ++n) {
+          const Col c0 = col_s[8 * n + 2 * t], c1 = col_s[8 * n + 2 * t + 1];
 #pragma unroll
-          for (int c = 0; c < NE; ++c) z[i][c] = fmaf(-slope[c], fabsf(col_pos[c] - pos), z[i][c]);
+          for (int i = 0; i < NI; ++i) {
+            const int pos = tb + g + 8 * i + 1;
+            z[i][n].x = fmaf(-c0.slope, fabsf((float)(c0.hi - pos)), z[i][n].x);
+            z[i][n].y = fmaf(-c1.slope, fabsf((float)(c1.hi - pos)), z[i][n].y);
+          }
         }
       }
       if constexpr (REC) {  // z + log2(s_v): what the weight is a power of
 #pragma unroll
         for (int i = 0; i < NI; ++i)
 #pragma unroll
-          for (int c = 0; c < NE; ++c) z[i][c] += vlg[i];
+          for (int n = 0; n < NT; ++n) z[i][n] = __fadd2_rn(z[i][n], make_float2(vlg[i], vlg[i]));
       }
       if (!inner) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int tk = g + 8 * i, pos = tb + tk;
+        for (int n = 0; n < NT; ++n) {
+          const Col c0 = col_s[8 * n + 2 * t], c1 = col_s[8 * n + 2 * t + 1];
 #pragma unroll
-          for (int c = 0; c < NE; ++c) {
-            const bool keep = (there >> tk & 1) && (pos < col_a[c] || (pos >= col_lo[c] && pos < col_hi[c]));
-            z[i][c] = keep ? z[i][c] : -CUDART_INF_F;
+          for (int i = 0; i < NI; ++i) {
+            const int tk = g + 8 * i, pos = tb + tk;
+            const bool have = there >> tk & 1;
+            z[i][n].x = have && (pos < c0.a || (pos >= c0.lo && pos < c0.hi)) ? z[i][n].x : -CUDART_INF_F;
+            z[i][n].y = have && (pos < c1.a || (pos >= c1.lo && pos < c1.hi)) ? z[i][n].y : -CUDART_INF_F;
           }
-          if constexpr (REC) vis[i] = vis[i] < CUDART_INF_F ? vis[i] : 1.f;  // beside a masked scale that is no number
+        }
+        if constexpr (REC) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) vis[i] = vis[i] < CUDART_INF_F ? vis[i] : 1.f;  // beside a masked scale that is no number
         }
       }
       bool grow = false;
-      float mx[NE];
+      float2 mx[NT];
 #pragma unroll
-      for (int c = 0; c < NE; ++c) {
-        mx[c] = z[0][c];
+      for (int n = 0; n < NT; ++n) {
+        mx[n] = z[0][n];
 #pragma unroll
-        for (int i = 1; i < NI; ++i) mx[c] = fmaxf(mx[c], z[i][c]);
-        grow = grow || mx[c] > m[c] + kSlack;
+        for (int i = 1; i < NI; ++i) mx[n] = make_float2(fmaxf(mx[n].x, z[i][n].x), fmaxf(mx[n].y, z[i][n].y));
+        grow = grow || mx[n].x > m[n].x + kSlack || mx[n].y > m[n].y + kSlack;
       }
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-        for (int c = 0; c < NE; ++c) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int sh = 4; sh <= 16; sh <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], sh));
-          const float mn = fmaxf(m[c], mx[c]);
-          const float alpha = mn > m[c] ? fast_exp2(m[c] - mn) : 1.f;
-          m[c] = mn;
-          l[c] *= alpha;
+          for (int sh = 4; sh <= 16; sh <<= 1) {
+            mx[n].x = fmaxf(mx[n].x, __shfl_xor_sync(0xffffffffu, mx[n].x, sh));
+            mx[n].y = fmaxf(mx[n].y, __shfl_xor_sync(0xffffffffu, mx[n].y, sh));
+          }
+          const float2 mn = make_float2(fmaxf(m[n].x, mx[n].x), fmaxf(m[n].y, mx[n].y));
+          const float2 alpha = make_float2(mn.x > m[n].x ? fast_exp2(m[n].x - mn.x) : 1.f,
+                                           mn.y > m[n].y ? fast_exp2(m[n].y - mn.y) : 1.f);
+          m[n] = mn;
+          l[n] = __fmul2_rn(l[n], alpha);
 #pragma unroll
           for (int jm = 0; jm < MT; ++jm) {
-            o[c / 2][jm][c % 2] *= alpha;
-            o[c / 2][jm][2 + c % 2] *= alpha;
+            o[n][jm][0] *= alpha.x; o[n][jm][1] *= alpha.y;
+            o[n][jm][2] *= alpha.x; o[n][jm][3] *= alpha.y;
           }
         }
       }
 #pragma unroll
-      for (int c = 0; c < NE; ++c) {
-        const float mu = m[c] == -CUDART_INF_F ? 0.f : m[c];
+      for (int n = 0; n < NT; ++n) {
+        const float2 nm = make_float2(m[n].x == -CUDART_INF_F ? 0.f : -m[n].x, m[n].y == -CUDART_INF_F ? 0.f : -m[n].y);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-          z[i][c] = fast_exp2(z[i][c] - mu);  // the weight; the probability is the weight / s_v
-          l[c] = REC ? fmaf(z[i][c], vis[i], l[c]) : l[c] + z[i][c];
+          const float2 d = __fadd2_rn(z[i][n], nm);
+          z[i][n] = make_float2(fast_exp2(d.x), fast_exp2(d.y));  // the weight; the probability is the weight / s_v
+          l[n] = REC ? ffma2(z[i][n], make_float2(vis[i], vis[i]), l[n]) : __fadd2_rn(l[n], z[i][n]);
         }
       }
 
       // rows of V that no column attends may hold anything: they become zero
       // (0 * NaN is NaN)
       uint32_t vkeep = 0xFFFFFFFFu;  // bit k: token k of the tile
-      if (!inner) vkeep = there & (low_bits(wk.c.a_max - tb) | (low_bits(any_hi - tb) & ~low_bits(any_lo - tb)));
+      if (!inner) vkeep = there & (low_bits(wk.c.a_max - tb) | (low_bits(wk.c.hi_max - tb) & ~low_bits(wk.c.lo_min - tb)));
 
 #pragma unroll
       for (int step = 0; step < STEPS; ++step) {
-        const uint8_t* vt = stage + GE::CACHE + step * GE::STEP;
         // ---- P^T as the B operand: columns = query rows, k = tokens
         uint32_t pb[NT][2], pr[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float w0 = z[2 * step + i][2 * n], w1 = z[2 * step + i][2 * n + 1];
-            const uint32_t h = BF ? pack_bf16x2(w0, w1) : pack_f16x2(w0, w1);
+            const float2 w = z[2 * step + i][n];
+            const uint32_t h = BF ? pack_bf16x2(w.x, w.y) : pack_f16x2(w.x, w.y);
             pb[n][i] = movmatrix_t(h);
             if constexpr (BF) {
               const float2 f = bf16x2_to_f2(h);
-              pr[n][i] = movmatrix_t(pack_bf16x2(w0 - f.x, w1 - f.y));
+              pr[n][i] = movmatrix_t(pack_bf16x2(w.x - f.x, w.y - f.y));
             }
           }
 
@@ -821,7 +934,7 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
 #pragma unroll
           for (int jm = 0; jm < MT; ++jm) {
             uint32_t r[4];
-            ldsm_x4_t(smem_addr(vt + chunk_at(vr, 2 * jm + vc)), r);
+            ldsm_x4_t(((stage + vx) ^ (uint32_t)(2 * jm % GE::CPB << 4)) + step * GE::R16 + 2 * jm / GE::CPB * (BS * GE::IB), r);
             if (!inner) {
               r[0] &= k0; r[1] &= k0; r[2] &= k1; r[3] &= k1;
             }
@@ -831,88 +944,84 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
               mma_k16_rows16<false>(o[n][jm], r[0], r[1], r[2], r[3], pr[n][0], pr[n][1]);
             }
           }
-        } else if constexpr (KIND == kFp4) {
-          constexpr int W = GE::DL / 8;  // words of a token row per lane: 2 or 1
-          uint32_t X[4][W], gv[2];
-          const int tk[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
-          uint32_t sc[4];
+        } else {
+          // the lane's dims of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+          constexpr int VB = KIND == kFp4 ? GE::DL / 2 : GE::DL, W = VB / 4;
+          uint32_t X[4][W];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int byte = g * (GE::DL / 2);  // within the row
-            const uint8_t* p = vt + chunk_at(tk[i], byte / 16) + byte % 16;
-            if constexpr (W == 2) {
-              const uint2 v = *reinterpret_cast<const uint2*>(p);
+            const uint32_t at = stage + (i % 2 ? vx1 : vx) + step * GE::R16 + i / 2 * GE::R8;
+            if constexpr (W == 4) {
+              const uint4 v = lds128(at);
+              X[i][0] = v.x; X[i][1] = v.y; X[i][2] = v.z; X[i][3] = v.w;
+            } else if constexpr (W == 2) {
+              const uint2 v = lds64(at);
               X[i][0] = v.x; X[i][1] = v.y;
             } else {
-              X[i][0] = *reinterpret_cast<const uint32_t*>(p);
+              X[i][0] = lds32(at);
             }
-            const int rr = tk[i] + 16 * step;
-            sc[i] = stage[GE::CACHE + (rr / BS) * GE::BLOCK + BS * GE::ROW + (rr % BS) * (D / 16) + g * GE::DL / 16];
-            if (!inner && !kept(tk[i])) sc[i] = 0u;  // an unwritten scale may be NaN
           }
-          gv[0] = e4m3x2_to_f16x2(sc[0] | sc[1] << 8);
-          gv[1] = e4m3x2_to_f16x2(sc[2] | sc[3] << 8);
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            // half byte k of a row's word is dim 8w + k: pair the tokens
-            uint32_t ev[2][4], od[2][4];  // [token pair][byte]: even dims, odd dims
+          if constexpr (KIND == kFp4) {
+            uint32_t gv[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              const uint32_t x0 = X[2 * p][w], x1 = X[2 * p + 1][w];
-              e2m1x8_to_f16x2x4((x0 & 0x0F0F0F0Fu) | (x1 << 4 & 0xF0F0F0F0u), ev[p]);
-              e2m1x8_to_f16x2x4((x0 >> 4 & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u), od[p]);
-#pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                ev[p][b] = hmul2(ev[p][b], gv[p]);
-                od[p][b] = hmul2(od[p][b], gv[p]);
+              const uint32_t at = stage + vg + step * GE::G16 + p * GE::G8;
+              uint32_t s0 = lds8(at), s1 = lds8(at + D / 16);
+              if (!inner) {  // an unwritten scale may be NaN
+                s0 = kept(2 * t + 8 * p) ? s0 : 0u;
+                s1 = kept(2 * t + 8 * p + 1) ? s1 : 0u;
               }
+              gv[p] = e4m3x2_to_f16x2(s0 | s1 << 8);
             }
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
+            for (int w = 0; w < W; ++w) {
+              // half byte k of a row's word is dim 8w + k: pair the tokens
+              uint32_t ev[2][4], od[2][4];  // [token pair][byte]: even dims, odd dims
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma_k16_rows16<true>(o[n][4 * w + b], ev[0][b], od[0][b], ev[1][b], od[1][b], pb[n][0], pb[n][1]);
-          }
-        } else {
-          constexpr int W = GE::DL / 4;  // words of a token row per lane: 4 or 2
-          uint32_t X[4][W];
-          const int tk[4] = {2 * t, 2 * t + 1, 2 * t + 8, 2 * t + 9};
+              for (int p = 0; p < 2; ++p) {
+                const uint32_t x0 = X[2 * p][w], x1 = X[2 * p + 1][w];
+                e2m1x8_to_f16x2x4((x0 & 0x0F0F0F0Fu) | (x1 << 4 & 0xF0F0F0F0u), ev[p]);
+                e2m1x8_to_f16x2x4((x0 >> 4 & 0x0F0F0F0Fu) | (x1 & 0xF0F0F0F0u), od[p]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int byte = g * GE::DL;
-            const uint8_t* p = vt + chunk_at(tk[i], byte / 16) + byte % 16;
-            if constexpr (W == 4) {
-              const uint4 v = *reinterpret_cast<const uint4*>(p);
-              X[i][0] = v.x; X[i][1] = v.y; X[i][2] = v.z; X[i][3] = v.w;
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(p);
-              X[i][0] = v.x; X[i][1] = v.y;
+                for (int b = 0; b < 4; ++b) {
+                  ev[p][b] = hmul2(ev[p][b], gv[p]);
+                  od[p][b] = hmul2(od[p][b], gv[p]);
+                }
+              }
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma_k16_rows16<true>(o[n][4 * w + b], ev[0][b], od[0][b], ev[1][b], od[1][b], pb[n][0], pb[n][1]);
             }
+          } else {
             if constexpr (KIND == kFp8) {
-              if (!inner && !kept(tk[i])) {  // an unwritten code may be NaN (int8 codes are numbers)
+              if (!inner) {  // an unwritten code may be NaN (int8 codes are numbers)
 #pragma unroll
-                for (int w = 0; w < W; ++w) X[i][w] = 0u;
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int w = 0; w < W; ++w) X[i][w] = kept(2 * t + 8 * (i / 2) + i % 2) ? X[i][w] : 0u;
               }
             }
-          }
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
-            // byte k of a row's word is dim 4w + k: pair the tokens, then widen
+            for (int w = 0; w < W; ++w) {
+              // byte k of a row's word is dim 4w + k: pair the tokens, then widen
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t sel = h ? 0x7362 : 0x5140;
-              const uint32_t p0 = __byte_perm(X[0][w], X[1][w], sel), p1 = __byte_perm(X[2][w], X[3][w], sel);
-              uint32_t a0, a1, a2, a3;
-              if constexpr (KIND == kFp8) {
-                e4m3x4_to_f16x2x2(p0, a0, a1);
-                e4m3x4_to_f16x2x2(p1, a2, a3);
-              } else {
-                i8x4_to_f16x2x2(p0, a0, a1);
-                i8x4_to_f16x2x2(p1, a2, a3);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = h ? 0x7362 : 0x5140;
+                const uint32_t p0 = __byte_perm(X[0][w], X[1][w], sel), p1 = __byte_perm(X[2][w], X[3][w], sel);
+                uint32_t a0, a1, a2, a3;
+                if constexpr (KIND == kFp8) {
+                  e4m3x4_to_f16x2x2(p0, a0, a1);
+                  e4m3x4_to_f16x2x2(p1, a2, a3);
+                } else {
+                  i8x4_to_f16x2x2(p0, a0, a1);
+                  i8x4_to_f16x2x2(p1, a2, a3);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                  mma_k16_rows16<true>(o[n][2 * w + h], a0, a1, a2, a3, pb[n][0], pb[n][1]);
               }
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma_k16_rows16<true>(o[n][2 * w + h], a0, a1, a2, a3, pb[n][0], pb[n][1]);
             }
           }
         }
@@ -924,16 +1033,19 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
 
     // ------------------------------------------------------------ piece end
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int sh = 4; sh <= 16; sh <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], sh);
-    if (wk.jb == 0 && wk.je == wk.nb) {
+      for (int sh = 4; sh <= 16; sh <<= 1) {
+        l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, sh);
+        l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, sh);
+      }
+    if (jb == 0 && je == wk.nb) {
       // the whole segment: the output rows
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         float inv[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) inv[e] = l[2 * n + e] == 0.f ? 0.f : a.out_scale / l[2 * n + e];
+        for (int e = 0; e < 2; ++e) inv[e] = (e ? l[n].y : l[n].x) == 0.f ? 0.f : a.out_scale / (e ? l[n].y : l[n].x);
         auto out_row = [&](int col) -> __nv_bfloat16* {
           const int r = wk.c.r0 + col;
           return a.out + (((int64_t)wk.c.q0 + r / a.group) * a.num_q_heads + wk.h * a.group + r % a.group) * D;
@@ -985,13 +1097,12 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
                   make_float4(o[n][jm][e], o[n][jm][2 + e], o[n][jm + 1][e], o[n][jm + 1][2 + e]);
           }
           if (g == 0) {
-            ps[NC * D + col] = m[2 * n + e];
-            ps[NC * D + NC + col] = l[2 * n + e];
+            ps[NC * D + col] = e ? m[n].y : m[n].x;
+            ps[NC * D + NC + col] = e ? l[n].y : l[n].x;
           }
         }
     }
-    ++piece;
-    wk = nx;
+    __syncwarp();  // the walk's slot is written again two pieces on
   }
 
   // Leave no copy in flight (only possible after a timeout).
@@ -999,80 +1110,95 @@ __global__ void __launch_bounds__(32, NT == 1 ? 12 : 8)
 }
 
 // ----------------------------------------------------------------------------
-// The merge of cut segments: CTA gw replays the plan of warp gw of a grid of
-// NW; when that warp's range starts inside a segment begun by earlier warps
-// and the segment ends within it, this CTA merges the segment's parts, one
-// column per warp at a time.
+// The merge of cut segments: CTA gw takes the one that warp gw of the attention
+// grid described, if any.  (A CTA per warp of that grid, of which few have
+// work, measured 2 to 4 us less than four CTAs per SM that look at several
+// descriptions each: a segment's merge is a chain of latencies, and segments
+// must not queue.)  The segment's columns are spread over the warps; where
+// there are fewer columns than warps, several warps share a column's parts.
 // ----------------------------------------------------------------------------
-constexpr int kMergeWarps = 4;
+inline int merge_warps(int cols) { return cols > 4 ? 8 : 4; }
 
-template <int D, int TOK, int NT>
-__global__ void __launch_bounds__(32 * kMergeWarps) merge_cols_kernel(const __grid_constant__ Args a, uint32_t NW) {
+template <int D, int NT>
+__global__ void __launch_bounds__(256) merge_cols_kernel(const __grid_constant__ Args a) {
   constexpr int NC = 8 * NT, SLOT = slot_floats(NC, D), V = D / 32;
+  const int MW = blockDim.x / 32;
+  constexpr int kRound = 8;  // parts in flight per warp
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  __shared__ float part_s[8][D + 2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t gw = blockIdx.x;
-  __shared__ Walk plan;
-  if (warp == 0) {
-    const Split split(total_tiles<NC, TOK>(a, lane), NW);
-    const uint32_t u0 = split.start(gw), u1 = split.start(gw + 1);
-    Walk w;
-    w.done = true;
-    if (u0 < u1) {
-      w = walk_from<NC, TOK>(a, u0, u1, lane);
-      if (!w.done && (w.jb == 0 || w.seg() + w.nb > u1)) w.done = true;
-      if (!w.done) {
-        // the segment's parts: `jb` becomes their number, `je` the first one's slot
-        const uint32_t first = split.owner(w.seg());
-        w.jb = (int)(gw - first + 1);
-        w.je = (int)(w.seg() != split.start(first) ? 2 * first + 1 : 2 * first);
-      }
-    }
-    if (lane == 0) plan = w;
-  }
-  __syncthreads();
-  const Walk w = plan;
-  // CTA 0 waits in any case, so that this grid never completes before the
-  // attention grid it depends on
-  if (!w.done || gw == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (w.done) return;
-  const int n = w.jb;
-  const uint32_t slot0 = (uint32_t)w.je, first = gw + 1 - n;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4* cp = reinterpret_cast<const int4*>(a.cuts + blockIdx.x);
+  const int4 c0 = __ldcg(cp), c1 = __ldcg(cp + 1);
+  const int n = c0.x, row0 = c0.w, r0 = c1.x, head0 = c1.z;
+  if (n == 0) return;
+  const uint32_t slot0 = (uint32_t)c0.y, first = (uint32_t)c0.z;
+  const int cols = min(NC, c1.y - r0);
+  const int share = cols >= MW ? 1 : MW / cols, at_once = MW / share;  // warps per column, columns at once
   auto part = [&](int i) -> const float* { return a.partials + (size_t)(i == 0 ? slot0 : 2 * (first + i)) * SLOT; };
-  const int rows = w.c.T * a.group;
-  for (int col = warp; col < NC && w.c.r0 + col < rows; col += kMergeWarps) {
-    float M = -CUDART_INF_F;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + NC * D + col));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (M == -CUDART_INF_F) M = 0.f;
-    float num[V], den = 0.f;
+  for (int base = 0; base < cols; base += at_once) {
+    const int col = base + warp / share, who = warp % share;
+    const bool have = col < cols && warp / share < at_once;
+    float num[V], den = 0.f, M = -CUDART_INF_F;
 #pragma unroll
     for (int d = 0; d < V; ++d) num[d] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* p = part(i);
-      const float f = fast_exp2(__ldcg(p + NC * D + col) - M);
-      den = fmaf(f, __ldcg(p + NC * D + NC + col), den);
-      if constexpr (V == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + col * D) + lane);
-        num[0] = fmaf(f, x.x, num[0]);
-        num[1] = fmaf(f, x.y, num[1]);
-        num[2] = fmaf(f, x.z, num[2]);
-        num[3] = fmaf(f, x.w, num[3]);
-      } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(p + col * D) + lane);
-        num[0] = fmaf(f, x.x, num[0]);
-        num[1] = fmaf(f, x.y, num[1]);
+    if (have) {
+      for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(part(i) + NC * D + col));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      if (M == -CUDART_INF_F) M = 0.f;
+      // parts who, who + share, ...: 32 factors at a time, one per lane
+      for (int i0 = who; i0 < n; i0 += 32 * share) {
+        const int i = i0 + lane * share;
+        float f = 0.f;
+        if (i < n) {
+          const float* p = part(i) + NC * D + col;
+          f = fast_exp2(__ldcg(p) - M);
+          den = fmaf(f, __ldcg(p + NC), den);
+        }
+        const int cnt = min(32, (n - i0 + share - 1) / share);
+        for (int k0 = 0; k0 < cnt; k0 += kRound) {
+          Vec x[kRound];
+#pragma unroll
+          for (int k = 0; k < kRound; ++k)
+            if (k0 + k < cnt) x[k] = __ldcg(reinterpret_cast<const Vec*>(part(i0 + (k0 + k) * share) + col * D) + lane);
+#pragma unroll
+          for (int k = 0; k < kRound; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+            if (k0 + k < cnt) {
+              const float* xv = reinterpret_cast<const float*>(&x[k]);
+#pragma unroll
+              for (int d = 0; d < V; ++d) num[d] = fmaf(fk, xv[d], num[d]);
+            }
+          }
+        }
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
     }
-    const float inv = den == 0.f ? 0.f : a.out_scale / den;
-    const int r = w.c.r0 + col;
-    __nv_bfloat16* dst =
-        a.out + (((int64_t)w.c.q0 + r / a.group) * a.num_q_heads + w.h * a.group + r % a.group) * D + V * lane;
-    if constexpr (V == 4) {
-      store4<__nv_bfloat16>(dst, num[0] * inv, num[1] * inv, num[2] * inv, num[3] * inv);
-    } else {
-      *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(num[0] * inv, num[1] * inv);
+    if (share > 1) {  // the column's shares, all relative to the same maximum
+#pragma unroll
+      for (int d = 0; d < V; ++d) part_s[warp][V * lane + d] = num[d];
+      if (lane == 0) part_s[warp][D] = den;
+      __syncthreads();
+      if (have && who == 0) {
+        for (int k = 1; k < share; ++k) {
+#pragma unroll
+          for (int d = 0; d < V; ++d) num[d] += part_s[warp + k][V * lane + d];
+          den += part_s[warp + k][D];
+        }
+      }
+      __syncthreads();
+    }
+    if (have && who == 0) {
+      const float inv = den == 0.f ? 0.f : a.out_scale / den;
+      const int r = r0 + col;
+      __nv_bfloat16* dst = a.out + ((int64_t)(row0 + r / a.group) * a.num_q_heads + head0 + r % a.group) * D + V * lane;
+      if constexpr (V == 4) {
+        store4<__nv_bfloat16>(dst, num[0] * inv, num[1] * inv, num[2] * inv, num[3] * inv);
+      } else {
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(num[0] * inv, num[1] * inv);
+      }
     }
   }
 }
@@ -1087,7 +1213,7 @@ struct Kernel {
 template <int KIND, int D, int BS, int NT>
 Kernel kernel_info() {
   return Kernel{reinterpret_cast<const void*>(&attn_cols_kernel<KIND, D, BS, NT>),
-                reinterpret_cast<const void*>(&merge_cols_kernel<D, Geo<KIND, D, BS>::TOK, NT>),
+                reinterpret_cast<const void*>(&merge_cols_kernel<D, NT>),
                 Smem<KIND, D, BS, NT>::kBytes, Geo<KIND, D, BS>::TOK};
 }
 

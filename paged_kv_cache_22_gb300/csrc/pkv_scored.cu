@@ -132,7 +132,8 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   a.prefix_lens = o.prefix_lens;
   a.window = o.window_tokens;
   a.sinks = o.window_tokens > 0 ? o.sink_tokens : 0;
-  a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounters);
+  a.cuts = reinterpret_cast<cols::Cut*>(static_cast<char*>(workspace) + kCounters);
+  a.partials = reinterpret_cast<float*>(a.cuts + (size_t)sms * max_ctas_per_sm(nt));
 
   TmaMaps maps{};
   if (takes_tiles(q_start && max_q > 1, rows, num_seqs, desc.num_kv_heads)) {
@@ -163,15 +164,14 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   // segments cut between warps are merged by a programmatic dependent grid
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(32 * cols::kMergeWarps);
+  cfg.blockDim = dim3(32 * cols::merge_warps((int)std::min<int64_t>(rows, nc)));
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  uint32_t warps = (uint32_t)grid;
-  void* margs[] = {&a, &warps};
+  void* margs[] = {&a};
   return cudaLaunchKernelExC(&cfg, k.merge, margs) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -192,7 +192,8 @@ size_t pkv_scored_workspace_bytes(int32_t num_seqs, int32_t max_q, int32_t num_q
   const int64_t rows = (int64_t)max_q * (num_q_heads / num_kv_heads);
   if (takes_tiles(max_q > 1, rows, num_seqs, num_kv_heads)) return kCounters;  // nothing is cut
   const int nt = column_tiles(rows);
-  return kCounters + (size_t)2 * sms * max_ctas_per_sm(nt) * cols::slot_floats(8 * nt, head_dim) * sizeof(float);
+  const size_t ctas = (size_t)sms * max_ctas_per_sm(nt);
+  return kCounters + ctas * sizeof(cols::Cut) + 2 * ctas * cols::slot_floats(8 * nt, head_dim) * sizeof(float);
 }
 
 pkv_status pkv_paged_attention_scored(void* out, const void* q, pkv_dtype q_dtype, const int32_t* q_start,
