@@ -154,8 +154,12 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
     dk.tensor_maps = true;
     if (!encode_cache_maps(dk, &desc, k_cache, v_cache, &maps)) return PKV_ERR_CUDA;
   }
-  // one wave of warps, no more than there are tiles
-  int64_t grid = (int64_t)sms * std::min(occ, max_ctas_per_sm(nt));
+  // one wave of warps, no more than there are tiles.  bf16 tiles: 7 warps per
+  // SM (128 sequences of up to 8192 tokens in 251 us; 11, as many as fit, 256:
+  // fewer copies queue at once); codes: as many as fit (8 x 32768 fp4 tokens:
+  // 88 us with 8 warps per SM, 76 with 16)
+  const int most = kind == cols::kBf16 && nt == 1 ? 7 : max_ctas_per_sm(nt);
+  int64_t grid = (int64_t)sms * std::min(occ, most);
   const int64_t tiles = num_seqs * chunks * desc.num_kv_heads * ((a.len_clip + k.tok - 1) / k.tok);
   if (tiles >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;  // the kernels count them in 32 bits
   grid = std::max<int64_t>(1, std::min(grid, tiles));

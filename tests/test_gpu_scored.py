@@ -304,6 +304,9 @@ def test_negative_and_zero_scale(pkv, kind):
     for scale in (-0.1, 0.0):
         p = Problem(pkv, kind, 64, 16, 4, 2, [70, 3], seed=3, scale=scale)
         p.check(p.run(softcap=4.0), *p.expected(softcap=4.0), f"{kind} {scale}")
+        p = Problem(pkv, kind, 64, 16, 4, 1, [170, 40], [60, 33], seed=3, scale=scale)
+        for o in ({}, dict(softcap=4.0)):
+            p.check(p.run(**o), *p.expected(**o), f"{kind} {scale} tiles")
 
 
 @pytest.mark.parametrize("kind", KINDS)
