@@ -80,6 +80,7 @@ struct Args {
   const float* slopes;
   const int32_t* prefix_lens;
   int window, sinks;
+  int by_length;    // 128-row tiles: the longest sequences first
   float* partials;  // [2 * CTAs][slot_floats(NC, D)]
   struct Cut* cuts; // [CTAs]
 };

@@ -2,6 +2,7 @@
 // pkv_paged_attention_quant: argument validation, the choice of kernel,
 // workspace and launches.
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <map>
 #include <mutex>
@@ -141,8 +142,12 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
     if (prepare(t.fn, tiles::kThreads, t.smem, dev) <= 0) return PKV_ERR_CUDA;
     if ((kind == cols::kBf16 || kind == cols::kFp8) && !encode_operand_maps(&desc, k_cache, v_cache, &maps))
       return PKV_ERR_CUDA;
-    const dim3 grid((unsigned)((rows + 2 * tiles::kTile - 1) / (2 * tiles::kTile)), (unsigned)desc.num_kv_heads,
-                    (unsigned)num_seqs);
+    const int64_t pairs = (rows + 2 * tiles::kTile - 1) / (2 * tiles::kTile) * desc.num_kv_heads;
+    if (pairs > INT_MAX) return PKV_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)pairs, 1, (unsigned)num_seqs);
+    // more than one wave: longest first, or a long sequence that starts late is
+    // what the call ends on
+    a.by_length = num_seqs > 1 && num_seqs <= 256 && pairs * num_seqs > sms;
     void* args[] = {&a, &maps};
     return cudaLaunchKernel(t.fn, grid, dim3(tiles::kThreads), args, t.smem, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   }

@@ -219,6 +219,42 @@ def test_tiles_of_query_rows(pkv, kind, shape, opt):
     assert pkv.get_device_error() == 0
 
 
+@pytest.mark.parametrize("rows", [32, 48])
+def test_tiles_of_many_long_sequences(pkv, rows):
+    """More CTAs than run at once, fed as fast as memory gives: K or V may come
+    late while the softmax is a step ahead of its products.  (128 and 192 rows
+    per kv head: CTAs of one tile and of two.)"""
+    hq, hkv, d, bs = 32, 8, 128, 16
+    lens = [2048 - 16 * ((37 * i) % 64) - i % 5 for i in range(64)]
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    tables, pool = tables_for(lens, bs, torch.Generator().manual_seed(rows))
+    n = sum(lens)
+    k, v = (torch.randn(n, hkv, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(64 * rows, hq, d, generator=g, device=DEV).to(torch.bfloat16)
+    kc = torch.full((pool, hkv, bs, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    vc = kc.clone()
+    pkv.kv_reshape_and_cache(k, v, kc, vc, slots_for(lens, tables, bs).to(DEV), 1.0)
+    q_start = torch.arange(65, dtype=torch.int32, device=DEV) * rows
+    out = torch.empty_like(q)
+    for _ in range(3):
+        out.fill_(7)
+        pkv.paged_attention_scored(out, q, kc, vc, tables.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                   1 / math.sqrt(d), q_start=q_start, max_q=rows, max_seq_len=2048)
+        assert pkv.get_device_error() == 0
+        at = 0
+        for s, L in enumerate(lens):
+            K, V = k[at: at + L].double(), v[at: at + L].double()
+            Q = q[s * rows: (s + 1) * rows].double().reshape(rows, hkv, hq // hkv, d)
+            z = torch.einsum("tkgd,nkd->tkgn", Q, K) / math.sqrt(d)
+            seen = torch.arange(L, device=DEV)[None] <= torch.arange(L - rows, L, device=DEV)[:, None]
+            w = torch.softmax(z.masked_fill(~seen[:, None, None], -math.inf), -1)
+            want = torch.einsum("tkgn,nkd->tkgd", w, V).reshape(rows, hq, d)
+            vmax = V.abs().amax((0, 2)).repeat_interleave(hq // hkv)[None, :, None]
+            over = (out[s * rows: (s + 1) * rows].double() - want).abs() - 2.0 ** -8 * want.abs() - (2.0 ** -8 + 2.0 ** -11) * vmax
+            assert over.max().item() <= 0, (s, L)
+            at += L
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_tiles_whose_maximum_grows(pkv, kind):
     """Scores that rise along the keys, by more than 2^8 between the halves of
