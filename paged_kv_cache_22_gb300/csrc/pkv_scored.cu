@@ -24,10 +24,24 @@ bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p
 // the 8-column instance, more the 16-column one.
 int column_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
-// Query rows of a (sequence, kv head) from which a call takes the 128-row tiles.
-constexpr int64_t kTileRows = 128;
-bool takes_tiles(bool several, int64_t rows, int num_seqs, int num_kv_heads) {
-  return several && rows >= kTileRows && num_seqs <= 65535 && num_kv_heads <= 65535;
+// Whether a call takes the 128-row tiles: `rows` query rows per (sequence, kv
+// head) at most.  The columns read K and V once per 16 rows but cut long
+// sequences between all SMs; the tiles read them once per 256 rows and leave
+// SMs idle when there are few (sequence, kv head) pairs.  So tiles when there
+// are enough 16-row chunks in all.  Times in us, columns / tiles, 8 kv heads, D
+// 128, for 64 sequences of 1024-2048 tokens and 4 of 2048-4096 (152 SMs: 608
+// chunks are 4 per SM):
+//   rows            32       64       128      192     | 4 seqs: 128    192
+//   bf16          132/97   235/98   414/101  591/132   |   55/50     73/71
+//   int8           98/151  170/152  313/156  455/192   |   52/92     70/115
+//   fp4            97/152  168/153  309/156  448/193   |   51/93     68/116
+// (fp8, D 64: 69/90, 120/91, 218/92, 316/115; 38/53, 50/65).  bf16 keeps the
+// columns below 128 rows, as pkv_paged_attention_multi does: they hold a weight
+// in 16 bits, the tiles in 8.
+bool takes_tiles(bool bf16, bool several, int64_t rows, int num_seqs, int num_kv_heads, int sms) {
+  const int64_t chunks = (rows + 15) / 16 * num_seqs * num_kv_heads;
+  return several && rows >= (bf16 ? 128 : 64) && chunks >= (bf16 ? 3 : 4) * sms && num_seqs <= 65535 &&
+         (rows + 2 * tiles::kTile - 1) / (2 * tiles::kTile) * num_kv_heads <= INT_MAX;
 }
 
 // CTAs per SM the workspace is sized for.
@@ -137,13 +151,12 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   a.partials = reinterpret_cast<float*>(a.cuts + (size_t)sms * max_ctas_per_sm(nt));
 
   TmaMaps maps{};
-  if (takes_tiles(q_start && max_q > 1, rows, num_seqs, desc.num_kv_heads)) {
+  if (takes_tiles(kind == cols::kBf16, q_start && max_q > 1, rows, num_seqs, desc.num_kv_heads, sms)) {
     const tiles::Kernel t = pick_tile_kernel(kind, D, bs);
     if (prepare(t.fn, tiles::kThreads, t.smem, dev) <= 0) return PKV_ERR_CUDA;
     if ((kind == cols::kBf16 || kind == cols::kFp8) && !encode_operand_maps(&desc, k_cache, v_cache, &maps))
       return PKV_ERR_CUDA;
     const int64_t pairs = (rows + 2 * tiles::kTile - 1) / (2 * tiles::kTile) * desc.num_kv_heads;
-    if (pairs > INT_MAX) return PKV_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)pairs, 1, (unsigned)num_seqs);
     // more than one wave: longest first, or a long sequence that starts late is
     // what the call ends on
@@ -199,7 +212,8 @@ size_t pkv_scored_workspace_bytes(int32_t num_seqs, int32_t max_q, int32_t num_q
   const int sms = pkv_device_sm_count();
   if (sms <= 0) return 0;
   const int64_t rows = (int64_t)max_q * (num_q_heads / num_kv_heads);
-  if (takes_tiles(max_q > 1, rows, num_seqs, num_kv_heads)) return kCounters;  // nothing is cut
+  if (takes_tiles(true, max_q > 1, rows, num_seqs, num_kv_heads, sms) && takes_tiles(false, max_q > 1, rows, num_seqs, num_kv_heads, sms))
+    return kCounters;  // nothing is cut, whatever the cache
   const int nt = column_tiles(rows);
   const size_t ctas = (size_t)sms * max_ctas_per_sm(nt);
   return kCounters + ctas * sizeof(cols::Cut) + 2 * ctas * cols::slot_floats(8 * nt, head_dim) * sizeof(float);

@@ -399,6 +399,65 @@ def test_masked_places_may_hold_anything(pkv, kind):
     assert torch.isnan(got).all()
 
 
+class Loose(Problem):
+    """Calls whose bound of query tokens is far above the rows: enough of them
+    for the 128-row tiles at any number of sequences."""
+
+    def run(self, *args, **kw):
+        if self.rows is not None and kw.get("max_q") is None:
+            kw["max_q"] = 1 << 14
+        return super().run(*args, **kw)
+
+
+@pytest.fixture
+def loose(monkeypatch):
+    monkeypatch.setitem(globals(), "Problem", Loose)
+
+
+@pytest.mark.parametrize("opt", list(OPTS))
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "d%d_bs%d_q%d_kv%d" % s)
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_at_a_loose_bound(pkv, loose, kind, shape, opt):
+    test_tiles_of_query_rows(pkv, kind, shape, opt)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_tile_cases_at_a_loose_bound(pkv, loose, kind):
+    test_long_chunk(pkv, kind)
+    test_verification_over_cut_segments(pkv, kind)
+    test_tiles_whose_maximum_grows(pkv, kind)
+    test_negative_and_zero_scale(pkv, kind)
+    for bs in (8, 32):
+        test_tiles_leave_out_bad_and_freed_blocks(pkv, kind, bs)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_tile_row_scales_and_queries_of_any_size(pkv, loose, kind):
+    """Prompt rows over K and V rows of very different sizes; query rows scaled
+    far down or up."""
+    def kv(k, v):
+        e = (torch.arange(k.shape[0]) * 7 % 41 - 20).float()
+        v = v * torch.exp2(e)[:, None, None] if kind in ("int8", "fp4") else v
+        v[::11] = 0
+        k[1::11] = 0
+        return k * torch.where(e < 0, 2.0, 0.5)[:, None, None], v
+
+    p = Problem(pkv, kind, 128, 16, 8, 2, [400, 70], [140, 37], seed=6, kv=kv)
+    p.check(p.run(), *p.expected(), kind)
+    p = Problem(pkv, kind, 64, 16, 8, 1, [150], [90], seed=2, scale=0.02)
+    p.q[:, 3] = (p.q[:, 3].float() * 1e-30).to(torch.bfloat16)
+    p.q[:, 5] = (p.q[:, 5].float() * 1e-4).to(torch.bfloat16)
+    p.check(p.run(), *p.expected(), kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("cap", [0.5, 12.0, 30.0, 80.0, 1e4, 1e30])
+def test_tiles_capped(pkv, loose, kind, cap):
+    """Scores far below the cap, near it and above: each form of the tanh."""
+    p = Problem(pkv, kind, 128, 16, 4, 1, [450, 300], [130, 70], seed=9)
+    p.check(p.run(softcap=cap), *p.expected(softcap=cap), f"{kind} {cap}")
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_bad_lengths(pkv, kind):
     """Decode: a negative length gives a zero row, one beyond the bound is
