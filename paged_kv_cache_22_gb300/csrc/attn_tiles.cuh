@@ -259,7 +259,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int na = (a_max + kStep - 1) / kStep, wt = lo_min / kStep;
   if (wt <= na) na = wt = 0;
   const int steps = nt - (wt - na);
-  auto base_of = [&](int j) -> int { return (j < na ? j : j + (wt - na)) * kStep; };
+  // First position of step j.  With a distance bias the last positions come
+  // first: scores then fall from step to step, where a steep slope would raise
+  // the maximum, and rescale O, at each (ragged prompts, 14 heads: 62 us instead of 51).
+  const bool backward = a.slopes != nullptr;
+  auto base_of = [&](int j) -> int {
+    const int i = backward ? steps - 1 - j : j;
+    return (i < na ? i : i + (wt - na)) * kStep;
+  };
   const int32_t* table = a.block_tables + (size_t)s * a.table_stride;
 
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sm + G::kBar);
@@ -580,9 +587,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kAll = NB == 32 ? 0xFFFFFFFFu : (1u << NB) - 1u;
       float m = -CUDART_INF_F;
       float2 l2 = f2(0.f);
-      // positions every row of the warp attends: [all_lo, all_hi)
+      // positions every row of the warp attends: [0, all_al) and [all_lo, all_hi)
       const int all_hi = __reduce_min_sync(0xffffffffu, my_row < 0 ? 0x7FFFFFFF : hi);
       const int all_lo = __reduce_max_sync(0xffffffffu, my_row < 0 ? 0 : lo);
+      const int all_al = __reduce_min_sync(0xffffffffu, my_row < 0 ? 0x7FFFFFFF : al);
       for (int j = 0; j < steps; ++j) {
         const int t0 = base_of(j), st = j % NS, cs = j % G::NCS, th = t0 + h * kHalf;  // first position of the step, of this half
         const uint32_t s_col = s_col0 + (j & 1) * kStep;
@@ -591,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         fence_after_sync();
         const uint32_t okb = ok_bits[j % kOkRing];
-        const bool inner = t0 >= all_lo && t0 + kStep <= all_hi && okb == kAll;  // no mask
+        const bool inner = ((t0 >= all_lo && t0 + kStep <= all_hi) || t0 + kStep <= all_al) && okb == kAll;  // no mask
         float v[kHalf];
         tmem_ld32(s_col, v);
         if constexpr (REC) {
@@ -623,8 +631,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (a.slopes) {  // z - slope |p - t|; p = hi - 1
           const float far = (float)(th - (hi - 1));
+          if (t0 + kStep <= all_hi) {  // t <= p: slope (t - p), packed
+            const float2 at = f2(slope * far);
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c) v[c] = fmaf(v[c], mul, -slope * fabsf(far + (float)c));
+            for (int c = 0; c < kHalf; c += 2) {
+              const float2 b = ffma2(f2(slope), make_float2((float)c, (float)(c + 1)), at);
+              const float2 e = ffma2(make_float2(v[c], v[c + 1]), f2(mul), b);
+              v[c] = e.x; v[c + 1] = e.y;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) v[c] = fmaf(v[c], mul, -slope * fabsf(far + (float)c));
+          }
           mul = 1.f;
         }
         if constexpr (REC) {
