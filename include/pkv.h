@@ -503,10 +503,13 @@ pkv_status pkv_copy_blocks(void* k_dst, void* v_dst, const pkv_cache_desc* dst, 
  *
  * A row x of largest magnitude a is stored as (all operations in binary32,
  * rounded to nearest even):
- *   PKV_QUANT_INT8   s = a / 127;  code = rint(x / s), value = code * s
- *   PKV_QUANT_FP4    s = a / 2688; per group of 16 elements of largest
+ *   PKV_QUANT_INT8   s = a * (1 / 127);  code = rint(x / s), value = code * s
+ *   PKV_QUANT_FP4    s = a * (1 / 2688); per group of 16 elements of largest
  *                    magnitude m, t = e4m3(m / (6 s)); code = e2m1(x / (t s))
  *                    (saturating at +-6), value = code * t * s
+ * with the constants 1 / 127 and 1 / 2688 rounded to binary32 first: what a
+ * tensor divided by a constant is in PyTorch on the GPU, so that such a program
+ * writes the same bytes.
  * A row with a < 2^-80 is stored as zeros; a row that holds an infinity or a
  * NaN is stored with a NaN scale and reads back as NaN.
  *

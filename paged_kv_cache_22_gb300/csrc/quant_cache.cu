@@ -124,7 +124,7 @@ constexpr float kMagic = 12583040.f;
 template <class R>
 __device__ __forceinline__ void int8_codes(const R& x, float s, uint32_t (&w)[4]) {
   const float inv = __frcp_rn(s);
-  // |x / s| <= 127 (1 + 2^-23), so that the quotient and the product are
+  // |x / s| <= 127 (1 + 2^-22), so that the quotient and the product are
   // within 2^-16 of each other.  (Ties are not rare: with bf16 elements
   // 127 x / a is a ratio of small whole numbers.)
   constexpr float kNear = 0.5f - 0x1p-15f;
@@ -185,7 +185,7 @@ __device__ __forceinline__ void store_run(const R& x, uint32_t row_max, uint32_t
   const bool bad = row_max >= 0x7F800000u;  // an infinity or a NaN in the row
   const float amax = __uint_as_float(row_max);
   const bool zero = bad || amax < kQuantTiny;
-  const float s = zero ? 0.f : __fdiv_rn(amax, FP4 ? 2688.f : 127.f);
+  const float s = zero ? 0.f : __fmul_rn(amax, FP4 ? 1.f / 2688.f : 1.f / 127.f);
   if constexpr (!FP4) {
     uint32_t w[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
     if (!zero) int8_codes(x, s, w);

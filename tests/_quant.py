@@ -30,8 +30,8 @@ def nearest_even(x: np.ndarray, table: np.ndarray) -> np.ndarray:
 
 
 def quantise_row(x: np.ndarray, fmt: str):
-    """(codes, group scale codes, row scale) of one binary32 row, the divisions
-    in binary32 as the format says."""
+    """(codes, group scale codes, row scale) of one binary32 row, the products
+    and divisions in binary32 as the format says."""
     x = x.astype(np.float32)
     D = x.size
     if not np.isfinite(x).all():
@@ -41,9 +41,9 @@ def quantise_row(x: np.ndarray, fmt: str):
     if a < TINY:
         return (np.full(D, 128, np.uint8) if fmt == "int8" else np.zeros(D, np.uint8)), np.zeros(D // 16, np.uint8), np.float32(0)
     if fmt == "int8":
-        s = np.float32(a / np.float32(127))
+        s = np.float32(a * np.float32(1 / 127))
         return (np.rint(x / s).astype(np.int32) + 128).astype(np.uint8), None, s
-    s = np.float32(a / np.float32(2688))
+    s = np.float32(a * np.float32(1 / 2688))
     table = e4m3_values()[:127]
     codes, groups = np.zeros(D, np.uint8), np.zeros(D // 16, np.uint8)
     for j in range(D // 16):
