@@ -33,8 +33,8 @@
 // for all of it: 550 us instead of 284 for the chunk below, MMAs waiting).
 //
 // Measured (8 sequences of 1024-4096 tokens, 512 query tokens each, 32 heads
-// on 8, D 128): 205 us for bf16 with a cap (840 TF/s; 44 % of what a large
-// library product reaches), 284 us for a 4-bit cache.  A step of 64 positions
+// on 8, D 128): 205 to 220 us for bf16 with a cap (785 to 840 TF/s; 43 % of what a large
+// library product reaches), 279 us for a 4-bit cache.  A step of 64 positions
 // takes some 2300 clocks, of which the two tiles' products need 1280 and the
 // softmax's arithmetic 1100 (exponents 512, multiply-adds and conversions the
 // rest); what is over is latency within a step that two warps per scheduler and
@@ -43,14 +43,15 @@
 // start first (247 us before they did, and before Q and O went through shared
 // memory in whole lines).
 //
-// softcap: cap * tanh(x / cap) through a cubic in (x / cap)^2 while every score
-// of a warp's step is below cap / 2 (relative error 6e-7), else through e^2u.
-// The cubic is evaluated where the exponent is formed: |cap * tanh(x / cap)| <=
+// softcap: cap * tanh(x / cap) through a quadratic in (x / cap)^2 while every
+// score of a warp's step is below cap / 4, a cubic below cap / 2 (relative error
+// 6e-7), else through e^2u.  (Below cap / 4 the cubic took 219 us, the quadratic
+// 205.)  They are evaluated where the exponent is formed: |cap * tanh(x / cap)| <=
 // |x| bounds the scores for the vote on the maximum.
 //
 // bf16 caches: tensor copies land in the operand layout, P is one bf16 operand
 // (a weight keeps 8 bits, as in pkv_paged_attention_multi: a remainder would
-// double the products; an output moves by at most 2^-9 max|V|).  Codes: raw
+// double the products; an output moves by at most 2^-8 max|V|).  Codes: raw
 // tiles land in a ring of steps of each cache, four warps widen them exactly; q
 // is fp16, each row scaled by a power of two (the factor goes to its scores); P
 // is one fp16 operand.  Row scales never touch the codes: K's multiplies the

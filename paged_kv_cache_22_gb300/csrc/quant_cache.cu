@@ -5,6 +5,10 @@
 // Both are bound by HBM: one pass over the data, each thread a run of 16
 // elements of one row (so that an fp4 group and its scale belong to one
 // thread), the 4 or 8 threads of a row joined by shuffles for its maximum.
+//
+// Measured, 262144 tokens of 8 kv heads, D 128, bf16: write fp4 308 us (1.39 GB,
+// 4.5 TB/s; conversions take half of the issue slots), int8 302 us; read-back
+// 243 us (5.7 TB/s) and 268 us.  The measured copy bandwidth is 6.7 TB/s.
 #include <cmath>
 
 #include "kernels.h"
