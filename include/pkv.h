@@ -580,8 +580,11 @@ pkv_status pkv_gather_kv_quant(void* k_out, void* v_out, pkv_dtype out_dtype, co
  *       or t < prefix_lens[s]
  *   out = sum_t softmax(z)_t V[t] over the attended t (a zero row if there is none)
  * A prefix is attended by every row of its sequence in both directions (a
- * prefix-LM's prompt) and through any window.  Zero-initialise the struct for
- * plain scores.
+ * prefix-LM's prompt) and through any window.  Positions that no row attends
+ * may hold anything.  A NaN or an infinity in the V of a bf16 or fp8 position
+ * that some rows of a call attend may reach the sequence's other rows of that
+ * kv head too (a weight of zero times it); a quantised row shows only where it
+ * is attended.  Zero-initialise the struct for plain scores.
  *   softcap       >= 0, finite; 0 = no cap
  *   alibi_slopes  device fp32 [num_q_heads], or NULL
  *   prefix_lens   device int32 [num_seqs], or NULL; a negative length is 0,

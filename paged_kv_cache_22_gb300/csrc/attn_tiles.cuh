@@ -253,7 +253,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int i0 = row0 / g, i1 = (min(row0 + 2 * kTile, rows) - 1) / g;
   const int hi_min = L - T + i0 + 1, hi_max = L - T + i1 + 1;
   const int lo_min = a.window > 0 ? max(0, hi_min - a.window) : 0;
-  const int lo_max = a.window > 0 ? max(0, hi_max - a.window) : 0;
   const int pre = a.prefix_lens ? min(max(__ldg(a.prefix_lens + s), 0), L) : 0;
   const int a_max = max(min(a.sinks, hi_max), pre);
   const int nt = (max(hi_max, a_max) + kStep - 1) / kStep;

@@ -178,8 +178,9 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   // 88 us with 8 warps per SM, 76 with 16)
   const int most = kind == cols::kBf16 && nt == 1 ? 7 : max_ctas_per_sm(nt);
   int64_t grid = (int64_t)sms * std::min(occ, most);
-  const int64_t tiles = num_seqs * chunks * desc.num_kv_heads * ((a.len_clip + k.tok - 1) / k.tok);
-  if (tiles >= ((int64_t)1 << 31)) return PKV_ERR_UNSUPPORTED;  // the kernels count them in 32 bits
+  const int64_t units = num_seqs * chunks * desc.num_kv_heads, each = (a.len_clip + (int64_t)k.tok - 1) / k.tok;  // (below 2^61)
+  if (units >= INT_MAX || units * each >= INT_MAX) return PKV_ERR_UNSUPPORTED;  // the kernels count tiles in 32 bits
+  const int64_t tiles = units * each;
   grid = std::max<int64_t>(1, std::min(grid, tiles));
   void* args[] = {&a, &maps};
   if (cudaLaunchKernel(k.fn, dim3((unsigned)grid), dim3(32), args, k.smem, st) != cudaSuccess) return PKV_ERR_CUDA;

@@ -459,6 +459,132 @@ def test_tiles_capped(pkv, loose, kind, cap):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_tiles_flag_bad_lengths(pkv, kind):
+    """The other sequences' rows are right, the bad ones' left as they were."""
+    lens, rows = [50, 30, 60], [3, 30, 9]
+    p = Loose(pkv, kind, 64, 16, 4, 2, lens, rows, seed=5)
+    want, vmax = p.expected()
+    at = [0, 3, 33, 42]
+    for ln in ([50, 7, 60], [50, -1, 60], [50, 10 ** 9, 60]):
+        got = p.run(lens=ln)
+        assert pkv.get_device_error() == pkv.DEVERR_BAD_SEQ_LEN
+        for s in range(3):
+            r = slice(at[s], at[s + 1])
+            if s == 1:
+                assert (got[r] == 7).all()
+            else:
+                p.check(got[r], want[r], vmax[r], f"{ln} sequence {s}")
+    for qs in ([0, 3, 33, 45], [0, 3, 1, 10], [-3, 3, 33, 42]):
+        got = p.run(q_start=torch.tensor(qs, dtype=torch.int32))
+        assert pkv.get_device_error() == pkv.DEVERR_BAD_SEQ_LEN
+        bad = [s for s in range(3) if qs[s] < 0 or qs[s + 1] < qs[s] or qs[s + 1] > 42]
+        touched = {r for s in range(3) if s not in bad for r in range(qs[s], qs[s + 1])}
+        assert all((got[r] == 7).all() for r in range(42) if r not in touched)
+    # padding rows behind the last sequence
+    p.q = torch.cat([p.q, p.q[:5]])
+    got = p.run()
+    p.check(got[:42], want[:42], vmax[:42])
+    assert (got[42:] == 7).all()
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_masked_places_may_hold_anything(pkv, kind):
+    """NaN and infinities at positions that no row of a chunk attends, in
+    blocks of which others are."""
+    lens, rows, W = [300, 130], [70, 40], 50
+    p = Loose(pkv, kind, 128, 16, 8, 2, lens, rows, seed=8)
+    opts = [dict(window=W), dict(window=W, sinks=2, alibi_slopes=slopes(8)), dict(window=W, softcap=30.0)]
+    wants = [p.expected(**o) for o in opts]
+    for s, L in enumerate(lens):
+        for t, x in ((2, "nan"), (5, "inf"), (L - rows[s] - W, "-inf"), (L - rows[s] - W - 1, "nan")):
+            slot = torch.tensor([int(p.tables[s, t // 16]) * 16 + t % 16], dtype=torch.int64, device=DEV)
+            x = torch.full((1, 2, 128), float(x), dtype=torch.bfloat16, device=DEV)
+            if kind in ("int8", "fp4"):
+                pkv.kv_quantize_and_cache(x, x, p.kc, p.vc, slot, 16, kind)
+            else:
+                pkv.kv_reshape_and_cache(x, x, p.kc, p.vc, slot, p.kv_scale)
+    for o, want in zip(opts, wants):
+        p.check(p.run(**o), *want, f"{kind} {o}")
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("max_q", [None, 1 << 14], ids=["columns", "tiles"])
+@pytest.mark.parametrize("kind", ["int8", "fp4"])
+def test_a_nan_row_shows_where_it_is_attended(pkv, kind, max_q):
+    """A quantised row of NaN: rows of a chunk before its position, or whose
+    window has left it, keep their values."""
+    L, T, W, bad = 120, 80, 30, 75
+    p = Problem(pkv, kind, 128, 16, 8, 2, [L], [T], seed=8)
+    want, vmax = p.expected(window=W)
+    x = torch.full((1, 2, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    slot = torch.tensor([int(p.tables[0, bad // 16]) * 16 + bad % 16], dtype=torch.int64, device=DEV)
+    pkv.kv_quantize_and_cache(x, x, p.kc, p.vc, slot, 16, kind)
+    seen = [r for r in range(T) if bad <= L - T + r < bad + W]
+    want[seen] = np.nan
+    p.check(p.run(max_q=max_q, window=W), want, vmax, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_tiles_of_many_short_sequences(pkv, kind):
+    """More sequences than are sorted by length; a few rows each, some none."""
+    g = torch.Generator().manual_seed(4)
+    lens = torch.randint(1, 40, (300,), generator=g).tolist()
+    rows = [min(n, r) for n, r in zip(lens, torch.randint(0, 6, (300,), generator=g).tolist())]
+    p = Problem(pkv, kind, 64, 8, 2, 1, lens, rows, seed=4)
+    p.check(p.run(max_q=100, softcap=6.0), *p.expected(softcap=6.0), kind)
+    assert pkv.get_device_error() == 0
+
+
+def test_tiles_streams_and_graphs(pkv):
+    """Calls on two streams at once, and two graphs replayed side by side with
+    inputs changed in between."""
+    ps = [Loose(pkv, "fp4", 128, 16, 8, 2, [700, 90, 5], [150, 40, 5], seed=1),
+          Loose(pkv, "bf16", 128, 16, 8, 2, [500, 300], [200, 1], seed=2)]
+    os = [dict(softcap=9.0), dict(window=100, alibi_slopes=slopes(8).to(DEV))]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    wants = [p.expected(**{k: v.cpu() if torch.is_tensor(v) else v for k, v in o.items()}) for p, o in zip(ps, os)]
+    torch.cuda.synchronize()
+    got = [[p.run(stream=st, **o) for p, o, st in zip(ps, os, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    for outs in got:
+        for p, x, want in zip(ps, outs, wants):
+            p.check(x, *want)
+
+    graphs = []
+    for p, o in zip(ps, os):
+        q, out = p.q.to(DEV), torch.zeros_like(p.q, device=DEV)
+        tb, ln, qs = p.tables.to(DEV), torch.tensor(p.lens, dtype=torch.int32, device=DEV), p.q_start.to(DEV)
+        kw = dict(q_start=qs, max_q=1 << 14, max_seq_len=max(p.lens), **o)
+
+        def call():
+            if p.kind == "fp4":
+                pkv.paged_attention_quant(out, q, p.kc, p.vc, tb, ln, p.scale, p.bs, p.kind, **kw)
+            else:
+                pkv.paged_attention_scored(out, q, p.kc, p.vc, tb, ln, p.scale, **kw)
+        call()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            call()
+        graphs.append((gr, q, out, tb, ln, qs))
+    for p, (_, q, *_) in zip(ps, graphs):
+        p.q = -p.q
+        q.copy_(p.q)
+    wants = [p.expected(**{k: v.cpu() if torch.is_tensor(v) else v for k, v in o.items()}) for p, o in zip(ps, os)]
+    for _ in range(5):
+        for gr in graphs:
+            gr[2].zero_()
+        torch.cuda.synchronize()
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr[0].replay()
+        torch.cuda.synchronize()
+        for p, gr, want in zip(ps, graphs, wants):
+            p.check(gr[2], *want)
+    assert pkv.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_bad_lengths(pkv, kind):
     """Decode: a negative length gives a zero row, one beyond the bound is
     clipped; several tokens: the sequence's rows are left as they were."""
