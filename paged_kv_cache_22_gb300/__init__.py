@@ -665,6 +665,12 @@ def scored_workspace_bytes(num_seqs: int, max_q: int, num_q_heads: int, num_kv_h
     return int(library().pkv_scored_workspace_bytes(num_seqs, max_q, num_q_heads, num_kv_heads, head_dim))
 
 
+@functools.lru_cache(maxsize=4096)
+def _scored_bytes(dev: int, *sizes: int) -> int:
+    """scored_workspace_bytes on device `dev`, which is the current one."""
+    return scored_workspace_bytes(*sizes)
+
+
 def _attend(call, what, desc, kv_scale, out, q, k_cache, v_cache, block_tables, seq_lens, scale, q_start, max_q, softcap,
             alibi_slopes, window, sinks, prefix_lens, max_seq_len, workspace, stream):
     shape = q.shape
@@ -695,7 +701,7 @@ def _attend(call, what, desc, kv_scale, out, q, k_cache, v_cache, block_tables, 
         rows = 1 if q_start is None else max_q
         if rows is None:
             rows = int((q_start[1:] - q_start[:-1]).max().item()) if B else 0
-        nbytes = scored_workspace_bytes(B, rows, Hq, desc.num_kv_heads, d)
+        nbytes = _scored_bytes(dev, B, rows, Hq, desc.num_kv_heads, d)
         # without a workspace of the caller's the call has one of its own: calls
         # on several streams and captured graphs then share nothing
         ws = (torch.empty(nbytes, dtype=torch.uint8, device=q.device) if workspace is None

@@ -6,9 +6,10 @@
 // elements of one row (so that an fp4 group and its scale belong to one
 // thread), the 4 or 8 threads of a row joined by shuffles for its maximum.
 //
-// Measured, 262144 tokens of 8 kv heads, D 128, bf16: write fp4 308 us (1.39 GB,
-// 4.5 TB/s; conversions take half of the issue slots), int8 302 us; read-back
-// 243 us (5.7 TB/s) and 268 us.  The measured copy bandwidth is 6.7 TB/s.
+// Measured, 262144 tokens of 8 kv heads, D 128, bf16: write fp4 289 us (1.39 GB,
+// 4.8 TB/s; conversions and maxima take two thirds of the issue slots; 308 us
+// with exact reciprocals and a division per group), int8 292 us; read-back 244
+// us (5.7 TB/s) and 271 us.  The measured copy bandwidth is 6.7 TB/s.
 #include <cmath>
 
 #include "kernels.h"
@@ -113,13 +114,24 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ uint32_t e2m1x8(const float* y) {
-  return e2m1x2(y[0], y[1]) | e2m1x2(y[2], y[3]) << 8 | e2m1x2(y[4], y[5]) << 16 | e2m1x2(y[6], y[7]) << 24;
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return r;
+}
+// 1 / x to one place (2^-23), for x and 1 / x normal.
+__device__ __forceinline__ float near_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // The codes are those of the binary32 quotient x / s.  A division costs about
 // ten instructions, more than everything else a run needs, and a product with
-// the reciprocal differs from it in the last place only: it is used wherever
-// that cannot change the code, that is, away from the borders between codes.
+// a reciprocal (itself a place off) differs from it by 2^-22 at most: it is used
+// wherever that cannot change the code, away from the borders between codes.
 // One run in a few thousand takes the division.
 
 // 1.5 * 2^23 + 128: a float whose unit is 1, with the biased code in its low byte.
@@ -127,9 +139,9 @@ constexpr float kMagic = 12583040.f;
 
 template <class R>
 __device__ __forceinline__ void int8_codes(const R& x, float s, uint32_t (&w)[4]) {
-  const float inv = __frcp_rn(s);
-  // |x / s| <= 127 (1 + 2^-22), so that the quotient and the product are
-  // within 2^-16 of each other.  (Ties are not rare: with bf16 elements
+  const float inv = near_rcp(s);
+  // |x / s| <= 127 (1 + 2^-22), so that the quotient and the (unrounded) product
+  // are within 127 (2^-23 + 2^-24) < 2^-15.4 of each other.  (Ties are not rare: with bf16 elements
   // 127 x / a is a ratio of small whole numbers.)
   constexpr float kNear = 0.5f - 0x1p-15f;
 #pragma unroll
@@ -158,7 +170,7 @@ template <class R>
 __device__ __forceinline__ void fp4_codes(const R& x, float step, uint32_t (&w)[2]) {
   // codes do not fall as the quotient grows: where a product a little below it
   // and one a little above (2^-21 either way) agree, it has that code too
-  const float inv = __frcp_rn(step), lo = inv * (1.f - 0x1p-21f), hi = inv * (1.f + 0x1p-21f);
+  const float inv = near_rcp(step), lo = inv * (1.f - 0x1p-21f), hi = inv * (1.f + 0x1p-21f);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float y[8], z[8];
@@ -197,7 +209,11 @@ __device__ __forceinline__ void store_run(const R& x, uint32_t row_max, uint32_t
   } else {
     uint32_t w[2] = {0u, 0u}, t = 0;
     if (!zero) {
-      t = __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(run_m), __fmul_rn(6.f, s)), __NV_SATFINITE, __NV_E4M3);
+      // the group scale, as the codes: by a product where both sides agree
+      const float m = __uint_as_float(run_m), s6 = __fmul_rn(6.f, s), u = m * near_rcp(s6);
+      const uint32_t both = __nv_cvt_float2_to_fp8x2(make_float2(u * (1.f - 0x1p-21f), u * (1.f + 0x1p-21f)), __NV_SATFINITE, __NV_E4M3);
+      t = both & 0xFFu;
+      if (t != both >> 8) t = __nv_cvt_float_to_fp8(__fdiv_rn(m, s6), __NV_SATFINITE, __NV_E4M3);
       __half_raw hr = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)t, __NV_E4M3);
       const float step = __fmul_rn(__half2float(*reinterpret_cast<__half*>(&hr)), s);
       if (step > 0.f) fp4_codes(x, step, w);

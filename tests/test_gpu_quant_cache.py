@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests._quant import quantise_row, read_row, slots_for, tables_for, write_row
+from tests._quant import e4m3_values, quantise_row, read_row, slots_for, tables_for, write_row
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -101,6 +101,32 @@ def test_codes_at_rounding_borders(pkv, fmt):
     pkv.kv_quantize_and_cache(x.to(DEV), (-x).contiguous().to(DEV), kc, vc, slots.to(DEV), bs, fmt)
     assert np.array_equal(kc.cpu().numpy(), expected(x, slots, shape, bs, fmt))
     assert np.array_equal(vc.cpu().numpy(), expected(-x, slots, shape, bs, fmt))
+
+
+@pytest.mark.parametrize("size", [1e-20, 1.0, 1e35])
+def test_group_scales_at_rounding_borders(pkv, size):
+    """Groups whose largest element puts m / (6 s) next to the middle between
+    two e4m3 codes (off by one unit in the last place of binary32)."""
+    d, bs, hkv, T = 128, 16, 2, 64
+    rng = np.random.default_rng(8)
+    grid = e4m3_values()[:127].astype(np.float32)
+    a = (rng.uniform(0.5, 1.0, (T, hkv, 1)) * size).astype(np.float32)
+    s6 = np.float32(6) * (a * np.float32(1 / 2688))
+    i = rng.integers(0, 126, (T, hkv, d // 16))
+    m = ((grid[i] + grid[i + 1]) / 2 * s6).astype(np.float32)
+    m = (m.view(np.int32) + rng.integers(-1, 2, m.shape, dtype=np.int32)).view(np.float32)
+    x = (rng.uniform(-1, 1, (T, hkv, d // 16, 16)).astype(np.float32) * m[..., None]).astype(np.float32)
+    x[..., 5] = m
+    x[:, :, 0, 0] = a[..., 0]
+    x = torch.from_numpy(x.reshape(T, hkv, d))
+    assert (x.abs().amax(-1) == torch.from_numpy(a[..., 0])).all()
+    slots = torch.arange(T, dtype=torch.int64)
+    shape = pkv.quant_cache_shape(T // bs, hkv, bs, d, "fp4")
+    kc = torch.full(shape, POISON, dtype=torch.uint8, device=DEV)
+    vc = torch.full_like(kc, POISON)
+    pkv.kv_quantize_and_cache(x.to(DEV), (-x).contiguous().to(DEV), kc, vc, slots.to(DEV), bs, "fp4")
+    assert np.array_equal(kc.cpu().numpy(), expected(x, slots, shape, bs, "fp4"))
+    assert np.array_equal(vc.cpu().numpy(), expected(-x, slots, shape, bs, "fp4"))
 
 
 @pytest.mark.parametrize("fmt", ["int8", "fp4"])
