@@ -17,10 +17,11 @@
 // is all that 512 columns of tensor memory hold, took 2630 clocks per 64.
 //
 // The maximum m of a row is lazy: it moves only when a score passes it by more
-// than 2^8 (weights stay below 2^8).  Each step the 256 threads of a tile vote
-// (one barrier with an OR) whether any row's must; the two threads of a row
-// exchange their maxima only then, and wait for the product before it only to
-// rescale O_x.
+// than 2^8 (weights stay below 2^8).  Each step the two warps of the same 32
+// rows vote (one barrier with an OR) whether any row's must; the two threads of
+// a row exchange their maxima only then, and wait for the product before it only
+// to rescale O_x.  (A vote of all 256 threads of a tile: 219 us instead of 214
+// for the bf16 chunk below.)
 //
 // Tensor memory: S_0, S_1 at columns 0 and 128 (two buffers of 64 each), O_0,
 // O_1 at 256 and 256 + D.
@@ -33,7 +34,7 @@
 // for all of it: 550 us instead of 284 for the chunk below, MMAs waiting).
 //
 // Measured (8 sequences of 1024-4096 tokens, 512 query tokens each, 32 heads
-// on 8, D 128): 205 to 220 us for bf16 with a cap (785 to 840 TF/s; 43 % of what a large
+// on 8, D 128): 200 to 214 us for bf16 with a cap (805 to 860 TF/s; 44 % of what a large
 // library product reaches), 279 us for a 4-bit cache.  A step of 64 positions
 // takes some 2300 clocks, of which the two tiles' products need 1280 and the
 // softmax's arithmetic 1100 (exponents 512, multiply-adds and conversions the
@@ -563,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---- the softmax threads: tile x, column half h, row r of the tile
     const int x = w >> 3, h = (w >> 2) & 1, r = (w & 3) * 32 + lane;
+    const int pair = 1 + x * 4 + (w & 3);  // barrier of the two warps of the same 32 rows
     if (x < nx) {
       int hi = 0, lo = 0, al = 0, my_row = -1, my_head = 0;
       const int R = row0 + x * kTile + r;
@@ -665,16 +667,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kHalf; ++c) v[c] = keep >> c & 1 ? v[c] : -CUDART_INF_F;
         }
         if (!late) mt = max32(v) * mul;
-        if (any_of(1 + x, 256, mt > m + cols::kSlack)) {
+        if (any_of(pair, 64, mt > m + cols::kSlack)) {
           if (late) {  // the bound was not enough: the scores themselves
             cap_series(v, k1);
             mt = max32(v) * mul;
             late = false;
           }
           xch[h * kTile + r] = mt;
-          asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + x) : "memory");
+          asm volatile("barrier.cta.sync %0, 64;" ::"r"(pair) : "memory");
           mt = fmaxf(mt, xch[(h ^ 1) * kTile + r]);
-          asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + x) : "memory");  // read before the next exchange
+          asm volatile("barrier.cta.sync %0, 64;" ::"r"(pair) : "memory");  // read before the next exchange
           float factor = 1.f;
           if (mt > m + cols::kSlack) {
             factor = m == -CUDART_INF_F ? 0.f : fast_exp2(m - mt);
@@ -769,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after_sync();
       const float mine = l2.x + l2.y;
       xch[h * kTile + r] = mine;
-      asm volatile("barrier.cta.sync %0, 256;" ::"r"(1 + x) : "memory");
+      asm volatile("barrier.cta.sync %0, 64;" ::"r"(pair) : "memory");
       const float l = mine + xch[(h ^ 1) * kTile + r];
       const float inv = l == 0.f ? 0.f : a.out_scale / l;
       // The rows go out through the tile's place in Q, which no product reads any
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
                          pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
       }
-      if (any_of(1 + x, 256, !ok)) ok = false;
+      if (any_of(9 + x, 256, !ok)) ok = false;
       if (ok) {
         constexpr int LPR = D / 8, RPI = 256 / LPR;
         const int c = lane % LPR;
