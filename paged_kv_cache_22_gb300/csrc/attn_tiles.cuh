@@ -31,11 +31,12 @@
 // MMA takes its issuing warp longer than the tensor pipe: one warp for both
 // tiles left the pipe idle); 16 and 18 the copies of K and V; 20-23 widen codes
 // to fp16 operands (fp8 and quantised caches), 32 rows of K or V each (two warps
-// for all of it: 550 us instead of 284 for the chunk below, MMAs waiting).
+// for all of it: 550 us instead of 284 for the chunk below, MMAs waiting; with all
+// of a warp's codes loaded before the first is widened 233).
 //
 // Measured (8 sequences of 1024-4096 tokens, 512 query tokens each, 32 heads
 // on 8, D 128): 200 to 214 us for bf16 with a cap (805 to 860 TF/s; 44 % of what a large
-// library product reaches), 279 us for a 4-bit cache.  A step of 64 positions
+// library product reaches), 233 us for a 4-bit cache.  A step of 64 positions
 // takes some 2300 clocks, of which the two tiles' products need 1280 and the
 // softmax's arithmetic 1100 (exponents 512, multiply-adds and conversions the
 // rest); what is over is latency within a step that two warps per scheduler and
@@ -396,35 +397,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ok = ok_bits[c * kOkRing + j % kOkRing] >> (half * BPG);
         uint8_t* const op = sm + (c ? G::kV : G::kK) + st * G::OP + (k / 4) * (kStep * kSpan) + 32 * half * kSpan;
         const uint8_t* const raws = sm + G::kRaw + ((c * NG + slot) * NB + half * BPG) * G::RAW;
-#pragma unroll 4
-        for (int u = 0; u < 16 / QPI; ++u) {
+        // all codes first: their loads' latency is paid once (a unit at a time,
+        // unrolled by four, the fp4 chunk took 279 us instead of 233)
+        constexpr int U = 16 / QPI;
+        uint4 y4[KIND == kFp4 ? 1 : U];
+        uint2 y2[KIND == kFp4 ? U : 1];
+        uint32_t ts[KIND == kFp4 ? U : 1];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
           const int rr = 2 * (u * QPI + q) ^ alt, p = rr % BS, b = rr / BS;  // row of the 32, of its block
           const uint8_t* raw = raws + b * G::RAW;
-          uint32_t h8[8];
           if constexpr (KIND == kFp4) {
-            const uint2 y = *reinterpret_cast<const uint2*>(raw + p * G::ROW + 16 * quant_chunk(p, k / 2, G::ROW) + 8 * (k & 1));
-            const uint32_t t = raw[BS * G::ROW + p * (D / 16) + k];
-            uint32_t f[4];
-            const uint32_t ts = cols::e4m3x2_to_f16x2(t | t << 8);
-            cols::e2m1x8_to_f16x2x4(y.x, f);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h8[e] = cols::hmul2(f[e], ts);
-            cols::e2m1x8_to_f16x2x4(y.y, f);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h8[4 + e] = cols::hmul2(f[e], ts);
+            y2[u] = *reinterpret_cast<const uint2*>(raw + p * G::ROW + 16 * quant_chunk(p, k / 2, G::ROW) + 8 * (k & 1));
+            ts[u] = raw[BS * G::ROW + p * (D / 16) + k];
           } else {
             constexpr int M = G::CPR - 1;
-            const uint4 y4 = *reinterpret_cast<const uint4*>(raw + p * G::ROW + ((k ^ ((p * G::ROW / 128) & M)) << 4));
-            const uint32_t y[4] = {y4.x, y4.y, y4.z, y4.w};
+            y4[u] = *reinterpret_cast<const uint4*>(raw + p * G::ROW + ((k ^ ((p * G::ROW / 128) & M)) << 4));
+          }
+        }
+        // V rows that no row attends, or that were not copied, are zero (0 * NaN
+        // is NaN); K rows may hold anything (their scores are masked)
+        const int first = base_of(j) + 32 * half;
+        const bool whole = !c || ((ok & ((1u << BPG) - 1)) == (1u << BPG) - 1 &&
+                                  (first + 32 <= a_max || (first >= lo_min && first + 32 <= hi_max)));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int rr = 2 * (u * QPI + q) ^ alt, b = rr / BS;
+          uint32_t h8[8];
+          if constexpr (KIND == kFp4) {
+            uint32_t f[4];
+            const uint32_t t2 = cols::e4m3x2_to_f16x2(ts[u] | ts[u] << 8);
+            cols::e2m1x8_to_f16x2x4(y2[u].x, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h8[e] = cols::hmul2(f[e], t2);
+            cols::e2m1x8_to_f16x2x4(y2[u].y, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h8[4 + e] = cols::hmul2(f[e], t2);
+          } else {
+            const uint32_t y[4] = {y4[u].x, y4[u].y, y4[u].z, y4[u].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               if constexpr (KIND == kFp8) e4m3x4_to_f16x2x2(y[e], h8[2 * e], h8[2 * e + 1]);
               else cols::i8x4_to_f16x2x2(y[e], h8[2 * e], h8[2 * e + 1]);
             }
           }
-          // V rows that no row attends, or that were not copied, are zero
-          // (0 * NaN is NaN); K rows may hold anything (their scores are masked)
-          if (c && (!(ok >> b & 1) || !wanted(base_of(j) + 32 * half + rr, 1))) {
+          if (!whole && (!(ok >> b & 1) || !wanted(first + rr, 1))) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) h8[e] = 0u;
           }

@@ -29,18 +29,18 @@ int column_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
 // sequences between all SMs; the tiles read them once per 256 rows and leave
 // SMs idle when there are few (sequence, kv head) pairs.  So tiles when there
 // are enough 16-row chunks in all.  Times in us, columns / tiles, 8 kv heads, D
-// 128, for 64 sequences of 1024-2048 tokens and 4 of 2048-4096 (152 SMs: 608
-// chunks are 4 per SM):
-//   rows            32       64       128      192     | 4 seqs: 128    192
-//   bf16          132/97   235/98   414/101  591/132   |   55/50     73/71
-//   int8           98/151  170/152  313/156  455/192   |   52/92     70/115
-//   fp4            97/152  168/153  309/156  448/193   |   51/93     68/116
-// (fp8, D 64: 69/90, 120/91, 218/92, 316/115; 38/53, 50/65).  bf16 keeps the
-// columns below 128 rows, as pkv_paged_attention_multi does: they hold a weight
-// in 16 bits, the tiles in 8.
+// 128, for 64 sequences of 1024-2048 tokens and 4 of 2048-4096 (3 chunks per SM
+// are 456 on 152 SMs; 4 x 8 x 192 rows are 384):
+//   rows       32       48       64       128      192    | 4 seqs: 128  192
+//   bf16     132/96   183/97   235/98   414/101  591/132  |    55/50   73/71
+//   int8      98/117  133/118  170/119  313/122  455/162  |    52/68   70/93
+//   fp4       97/119  132/120  168/120  309/123  448/162  |    51/69   68/93
+// (fp8, D 64: 69/87, 95/88, 120/88, 218/89, 316/115; 38/49, 50/65).  Codes gain
+// from 48 rows on; bf16 keeps the columns below 128, as
+// pkv_paged_attention_multi does: they hold a weight in 16 bits, the tiles in 8.
 bool takes_tiles(bool bf16, bool several, int64_t rows, int num_seqs, int num_kv_heads, int sms) {
   const int64_t chunks = (rows + 15) / 16 * num_seqs * num_kv_heads;
-  return several && rows >= (bf16 ? 128 : 64) && chunks >= (bf16 ? 3 : 4) * sms && num_seqs <= 65535 &&
+  return several && rows >= (bf16 ? 128 : 48) && chunks >= 3 * sms && num_seqs <= 65535 &&
          (rows + 2 * tiles::kTile - 1) / (2 * tiles::kTile) * num_kv_heads <= INT_MAX;
 }
 
