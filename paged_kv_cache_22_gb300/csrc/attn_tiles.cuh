@@ -35,8 +35,8 @@
 // of a warp's codes loaded before the first is widened 233).
 //
 // Measured (8 sequences of 1024-4096 tokens, 512 query tokens each, 32 heads
-// on 8, D 128): 200 to 214 us for bf16 with a cap (805 to 860 TF/s; 44 % of what a large
-// library product reaches), 233 us for a 4-bit cache.  A step of 64 positions
+// on 8, D 128): 195 to 209 us for bf16 with a cap (825 to 885 TF/s; 45 % of what a large
+// library product reaches), 229 us for a 4-bit cache.  A step of 64 positions
 // takes some 2300 clocks, of which the two tiles' products need 1280 and the
 // softmax's arithmetic 1100 (exponents 512, multiply-adds and conversions the
 // rest); what is over is latency within a step that two warps per scheduler and
@@ -76,7 +76,6 @@ using cols::kInt8;
 constexpr int kStep = 64;       // positions per step
 constexpr int kHalf = 32;       // columns of S per softmax thread
 constexpr int kTile = 128;      // query rows per tile (TMEM lanes)
-constexpr int kThreads = 768;
 constexpr int kSpan = 128;      // bytes of a swizzle span
 constexpr int kMaxSmem = 232448;
 constexpr int kOkRing = 16;     // steps whose block bits are kept (more than the copies run ahead)
@@ -86,6 +85,9 @@ struct Geo {
   static constexpr bool BF = KIND == kBf16;
   static constexpr bool REC = KIND == kInt8 || KIND == kFp4;
   static constexpr int SPANS = D / 64;
+  // bf16 has no warps that widen codes, and more registers for the rest (95 for
+  // 80: the chunk above 215 -> 209 us)
+  static constexpr int kThreads = BF ? 640 : 768;
   static constexpr int NB = kStep / BS;                       // blocks per step
   static constexpr int OP = SPANS * kStep * kSpan;            // one operand tile of K or V
   static constexpr int NS = BF ? (D == 128 ? 4 : 8) : 3;      // operand stages of K, of V
@@ -209,7 +211,7 @@ __device__ __forceinline__ float maxabs32(const float (&v)[32]) {
 }
 
 template <int KIND, int D, int BS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Geo<KIND, D, BS>::kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ Args a, const __grid_constant__ TmaMaps maps) {
   using namespace tc05;
   using G = Geo<KIND, D, BS>;
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + G::kTmem);
   int s = blockIdx.z;
   if (a.by_length) {  // CTAs start in the order of their index: the longest sequences come first
-    for (int i = tid; i < a.num_seqs; i += kThreads) {
+    for (int i = tid; i < a.num_seqs; i += G::kThreads) {
       const int n = __ldg(a.seq_lens + i);
       int rank = 0;
       for (int k = 0; k < a.num_seqs; ++k) {
@@ -620,12 +622,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t okb = ok_bits[j % kOkRing];
         const bool inner = ((t0 >= all_lo && t0 + kStep <= all_hi) || t0 + kStep <= all_al) && okb == kAll;  // no mask
         float v[kHalf];
-        tmem_ld32(s_col, v);
+        float4 kpre[REC ? kHalf / 4 : 1];  // (before S: their latency hides behind its load, 232 -> 228 us)
         if constexpr (REC) {
           const float4* ks = reinterpret_cast<const float4*>(ksc_s + cs * kStep + kHalf * h);
 #pragma unroll
+          for (int c = 0; c < kHalf / 4; ++c) kpre[c] = ks[c];
+        }
+        tmem_ld32(s_col, v);
+        if constexpr (REC) {
+#pragma unroll
           for (int c = 0; c < kHalf / 4; ++c) {
-            const float4 k4 = ks[c];
+            const float4 k4 = kpre[c];
             const float2 e = __fmul2_rn(make_float2(v[4 * c], v[4 * c + 1]), make_float2(k4.x, k4.y));
             const float2 f = __fmul2_rn(make_float2(v[4 * c + 2], v[4 * c + 3]), make_float2(k4.z, k4.w));
             v[4 * c] = e.x; v[4 * c + 1] = e.y; v[4 * c + 2] = f.x; v[4 * c + 3] = f.y;
@@ -829,12 +836,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 struct Kernel {
   const void* fn = nullptr;
-  int smem = 0;
+  int smem = 0, threads = 0;
 };
 
 template <int KIND, int D, int BS>
 Kernel kernel_info() {
-  return Kernel{reinterpret_cast<const void*>(&attn_tiles_kernel<KIND, D, BS>), Geo<KIND, D, BS>::kBytes};
+  using G = Geo<KIND, D, BS>;
+  return Kernel{reinterpret_cast<const void*>(&attn_tiles_kernel<KIND, D, BS>), G::kBytes, G::kThreads};
 }
 
 template <int KIND>

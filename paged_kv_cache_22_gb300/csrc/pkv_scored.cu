@@ -153,7 +153,7 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
   TmaMaps maps{};
   if (takes_tiles(kind == cols::kBf16, q_start && max_q > 1, rows, num_seqs, desc.num_kv_heads, sms)) {
     const tiles::Kernel t = pick_tile_kernel(kind, D, bs);
-    if (prepare(t.fn, tiles::kThreads, t.smem, dev) <= 0) return PKV_ERR_CUDA;
+    if (prepare(t.fn, t.threads, t.smem, dev) <= 0) return PKV_ERR_CUDA;
     if ((kind == cols::kBf16 || kind == cols::kFp8) && !encode_operand_maps(&desc, k_cache, v_cache, &maps))
       return PKV_ERR_CUDA;
     const int64_t pairs = (rows + 2 * tiles::kTile - 1) / (2 * tiles::kTile) * desc.num_kv_heads;
@@ -162,7 +162,7 @@ pkv_status attend(int kind, const pkv_cache_desc& desc, void* out, const void* q
     // what the call ends on
     a.by_length = num_seqs > 1 && num_seqs <= 256 && pairs * num_seqs > sms;
     void* args[] = {&a, &maps};
-    return cudaLaunchKernel(t.fn, grid, dim3(tiles::kThreads), args, t.smem, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return cudaLaunchKernel(t.fn, grid, dim3(t.threads), args, t.smem, st) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   }
   const cols::Kernel k = pick_kernel(kind, D, bs, nt);
   const int occ = prepare(k.fn, 32, k.smem, dev);
