@@ -35,9 +35,9 @@
 // of a warp's codes loaded before the first is widened 233).
 //
 // Measured (8 sequences of 1024-4096 tokens, 512 query tokens each, 32 heads
-// on 8, D 128): 195 to 209 us for bf16 with a cap (825 to 885 TF/s; 45 % of what a large
+// on 8, D 128): 209 us for bf16 with a cap (827 TF/s; 43 % of what a large
 // library product reaches), 229 us for a 4-bit cache.  A step of 64 positions
-// takes some 2300 clocks, of which the two tiles' products need 1280 and the
+// takes some 2200 clocks, of which the two tiles' products need 1280 and the
 // softmax's arithmetic 1100 (exponents 512, multiply-adds and conversions the
 // rest); what is over is latency within a step that two warps per scheduler and
 // tile do not hide.  Each CTA adds 3 us before its first product, and CTAs of
